@@ -88,8 +88,9 @@ def parse():
 # Sources that make up each kernel: a measured traffic figure is only used
 # while they are unchanged.
 KERNEL_SOURCES = {
-    "decode": ["unstructured_sparse_weight_amd/csrc/usw_spmm.hip", "unstructured_sparse_weight_amd/csrc/usw_decode_common.h",
-               "unstructured_sparse_weight_amd/csrc/usw_device.h"],
+    "decode": ["unstructured_sparse_weight_amd/csrc/usw_spmm.hip", "unstructured_sparse_weight_amd/csrc/usw_decode_plan.h",
+               "unstructured_sparse_weight_amd/csrc/usw_decode_kernels.h",
+               "unstructured_sparse_weight_amd/csrc/usw_decode_common.h", "unstructured_sparse_weight_amd/csrc/usw_device.h"],
     "union": ["unstructured_sparse_weight_amd/csrc/usw_union.hip", "unstructured_sparse_weight_amd/csrc/usw_decode_common.h",
               "unstructured_sparse_weight_amd/csrc/usw_device.h"],
     "cbc": ["unstructured_sparse_weight_amd/csrc/usw_cbc.hip", "unstructured_sparse_weight_amd/csrc/usw_device.h"],

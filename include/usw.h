@@ -88,6 +88,13 @@ typedef int32_t usw_status;
 #define USW_OUT_F16 1             /* Y in fp16 */
 #define USW_OUT_F32 3             /* Y in fp32 */
 
+/* Activations of the products with an epilogue. */
+#define USW_ACT_NONE 0
+#define USW_ACT_RELU 1
+#define USW_ACT_GELU 2            /* v (1 + erf(v / sqrt 2)) / 2 */
+#define USW_ACT_GELU_TANH 3       /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+#define USW_ACT_SILU 4            /* v / (1 + exp(-v)) */
+
 /* Non-owning view of one encoded matrix.  For usw_spmm every pointer is a
  * device pointer; for usw_validate every pointer is a host pointer. */
 typedef struct usw_fmt {
@@ -620,6 +627,127 @@ usw_status usw_cbc_spmspv_workspace(const usw_cbc_fmt* fmt, int32_t splits, size
  */
 usw_status usw_cbc_spmspv(const usw_cbc_fmt* fmt, const uint16_t* x, void* y, int32_t y_type, float tau,
                           int32_t splits, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The product with an epilogue, of one weight and by expert.
+ *
+ *   y[n][m] = res[n][m] + mul[n][m] * act(sum_k W_sp[m][k] x[n][k] + bias[m])
+ *
+ * for the TCA-BME format (fp16 or INT4 values, 64x64 GroupTiles).  The sums
+ * are fp32 and so is the epilogue; y is rounded once.  A feed-forward block
+ * is made of these: OPT's relu(W1 x + b1) and W2 h + b2 + residual, or
+ * Llama's silu(Wg x) * (Wu x), where mul is the other projection's output.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct usw_epilogue {
+  const uint16_t* bias;  /* fp16 [M] (by expert: [E][M]) or NULL */
+  const uint16_t* mul;   /* fp16 [rows][ld_mul] or NULL */
+  const uint16_t* res;   /* fp16 [rows][ld_res] or NULL */
+  int64_t ld_mul;        /* row strides in elements, multiples of 8; 0 = M */
+  int64_t ld_res;
+  int32_t act;           /* USW_ACT_* */
+  int32_t reserved;      /* must be 0 */
+} usw_epilogue;
+
+/*
+ * Workspace of usw_spmm_fused (0 when none) and its leading counter bytes,
+ * with usw_spmm_ex's rules: the counters must be zero when a call starts and
+ * are zero again when it ends, and calls that may overlap need workspaces of
+ * their own.
+ */
+usw_status usw_spmm_fused_workspace(const usw_fmt* fmt, int32_t N, int32_t splits, size_t* bytes,
+                                    size_t* counter_bytes);
+
+/*
+ * Y [N][M] as above, X [N][K] fp16.  As usw_spmm_ex otherwise (layouts,
+ * alignment, splits, workspace, stream, determinism).  ep may be NULL: no
+ * epilogue.  ep and the struct it points to are read during the call.  Y may
+ * be the residual itself (same address, ld_res = M); it may overlap nothing
+ * else that the call reads.
+ * Errors: as usw_spmm_ex, and BAD_DTYPE (act), BAD_SHAPE (a stride below M or
+ * above 2^31, reserved), MISALIGNED (scales, bias, mul or res not 16-byte
+ * aligned, a stride that is no multiple of 8).
+ */
+usw_status usw_spmm_fused(const usw_fmt* fmt, const uint16_t* X, void* Y, int32_t y_type, int32_t N,
+                          const usw_epilogue* ep, int32_t splits, void* ws, size_t ws_bytes, void* stream);
+
+/* Non-owning view of E encodings of one shape and value type, one after the
+ * other (device pointers).  GroupTiles are 64x64. */
+typedef struct usw_expert_fmt {
+  int32_t E, M, K;
+  int32_t val_type;         /* USW_VAL_F16 or USW_VAL_I4 */
+  int32_t reserved;         /* must be 0 */
+  int64_t nnz;              /* kept elements of all experts */
+  int64_t values_bytes;     /* size of values: the sum of the experts' padded sizes */
+  const uint64_t* bitmaps;  /* [E][M*K/64] */
+  const uint32_t* offsets;  /* [E][NGT+1], each expert's from 0 */
+  const void* values;       /* the experts' padded values (usw_encode_query's values_alloc) */
+  const int64_t* starts;    /* [E+1] byte offset of each expert's values, multiples of 16 */
+  const uint16_t* scales;   /* I4: fp16 [E][M]; F16: ignored */
+} usw_expert_fmt;
+
+usw_status usw_expert_spmm_workspace(const usw_expert_fmt* fmt, int32_t S, size_t* bytes, size_t* counter_bytes);
+
+/*
+ * The product by expert: row s of Y [S][M] is the product of expert e's
+ * weight for slots[e] <= s < slots[e+1].
+ *   X:     fp16 [T][K].  Slot s reads row rows[s], or row s when rows is NULL
+ *          (then T >= S).
+ *   slots: device int32 [E+1], non-decreasing from 0 to at most S.  Read on
+ *          the device: the host needs only the bound S (usw_expert_route's
+ *          T * k).  Rows of Y from slots[E] on are left as they were.
+ *   rows:  device int32 [S] or NULL; entries from slots[E] on are not read.
+ *   ep:    as usw_spmm_fused, with a bias per expert; mul and res have a row
+ *          per slot.
+ * Runs, rows and starts are clamped to the buffers: wrong ones give wrong
+ * rows, not wrong accesses.  S = 0 does nothing.
+ * Errors: as usw_spmm_fused; BAD_N (S or T negative, T < S without rows, T = 0
+ * with S > 0), BAD_SHAPE (E < 1, nnz or values_bytes impossible), UNSUPPORTED
+ * (E > 1024).
+ */
+usw_status usw_expert_spmm(const usw_expert_fmt* fmt, const uint16_t* X, int32_t T, const int32_t* slots,
+                           const int32_t* rows, int32_t S, void* Y, int32_t y_type, const usw_epilogue* ep, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* Workspace of usw_expert_route (need not be initialised; 0 up to 256 tokens). */
+usw_status usw_expert_route_workspace(int32_t T, int32_t E, int32_t k, size_t* bytes);
+
+/*
+ * Routing: of each token's E logits the k largest are chosen (of equal ones
+ * the lower expert), never -inf or NaN, so a token may get fewer than k
+ * experts, or none.  The weights are softmax values: over the chosen experts
+ * (renormalize nonzero) or over all of them.  The chosen pairs, the slots,
+ * are sorted by (expert, token).
+ *   logits:  [T][ld] fp16 (l_type USW_OUT_F16) or fp32 (USW_OUT_F32); ld 0 = E.
+ *   ids:     out int32 [T][k], the chosen experts, largest logit first; -1
+ *            where none was left.
+ *   weights: out fp32 [T][k]; 0 where none was left.
+ *   slots:   out int32 [E+1], the first slot of each expert; slots[E] slots in all.
+ *   rows:    out int32 [T k], the token of each slot; -1 from slots[E] on.
+ *   pos:     out int32 [T][k], the slot of each choice; -1 where none was left.
+ * Deterministic.  T = 0 writes slots only.
+ * Errors: NULL_ARG, BAD_N (T < 0), BAD_SHAPE (E < 1, k < 1, k > E, ld < E or
+ * > 2^31), BAD_DTYPE, UNSUPPORTED (E > 1024, k > 16, T k >= 2^31),
+ * MISALIGNED, WORKSPACE, HIP.
+ */
+usw_status usw_expert_route(const void* logits, int32_t l_type, int64_t ld, int32_t T, int32_t E, int32_t k,
+                            int32_t renormalize, int32_t* ids, float* weights, int32_t* slots, int32_t* rows,
+                            int32_t* pos, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * out[t][m] = res[t][m] + sum over j of weights[t][j] * Y[pos[t][j]][m], added
+ * in the order of j in fp32 and rounded once.
+ *   Y:   [S][M] fp16 or fp32, 16-byte aligned, M a multiple of 8.
+ *   pos: int32 [T][k]; a negative slot, or one of S or more, counts nothing.
+ *   res: fp16 [T][ld_res] or NULL (ld_res a multiple of 8, 0 = M); out may be
+ *        res itself when out is fp16 and ld_res = M.
+ *   out: [T][M] fp16 or fp32, 16-byte aligned.
+ * Errors: NULL_ARG, BAD_N, BAD_SHAPE, BAD_DTYPE, MISALIGNED, UNSUPPORTED, HIP.
+ */
+usw_status usw_expert_combine(const void* Y, int32_t y_type, int32_t S, int32_t M, const int32_t* pos,
+                              const float* weights, int32_t T, int32_t k, const uint16_t* res, int64_t ld_res,
+                              void* out, int32_t out_type, void* stream);
 
 /*
  * Measurement utility, not part of the SpMM path: reads the first

@@ -19,6 +19,7 @@ USW_VAL_I4 = 2
 USW_VAL_I2 = 3
 USW_OUT_F16 = 1
 USW_OUT_F32 = 3
+USW_ACT = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 STATUS_NAMES = {
     0: "OK", -1: "NULL_ARG", -2: "BAD_SHAPE", -3: "BAD_DTYPE", -4: "BAD_N", -5: "UNSUPPORTED",
@@ -37,6 +38,8 @@ EXPORTED = (
     "usw_union_spmm_counter_bytes", "usw_union_spmm",
     "usw_cbc_encode_query", "usw_cbc_encode", "usw_cbc_validate",
     "usw_cbc_encode_device_index", "usw_cbc_encode_device_values", "usw_cbc_spmspv_workspace", "usw_cbc_spmspv",
+    "usw_spmm_fused_workspace", "usw_spmm_fused", "usw_expert_spmm_workspace", "usw_expert_spmm",
+    "usw_expert_route_workspace", "usw_expert_route", "usw_expert_combine",
 )
 
 
@@ -81,6 +84,26 @@ class UswCbcFmt(ctypes.Structure):
         ("nnz_padded", ctypes.c_int64),
         ("bitmaps", ctypes.c_void_p), ("tile_offsets", ctypes.c_void_p),
         ("colinfo", ctypes.c_void_p), ("values", ctypes.c_void_p),
+    ]
+
+
+class UswEpilogue(ctypes.Structure):
+    """Mirror of ``usw_epilogue``."""
+    _fields_ = [
+        ("bias", ctypes.c_void_p), ("mul", ctypes.c_void_p), ("res", ctypes.c_void_p),
+        ("ld_mul", ctypes.c_int64), ("ld_res", ctypes.c_int64),
+        ("act", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class UswExpertFmt(ctypes.Structure):
+    """Mirror of ``usw_expert_fmt``."""
+    _fields_ = [
+        ("E", ctypes.c_int32), ("M", ctypes.c_int32), ("K", ctypes.c_int32),
+        ("val_type", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("nnz", ctypes.c_int64), ("values_bytes", ctypes.c_int64),
+        ("bitmaps", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+        ("values", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("scales", ctypes.c_void_p),
     ]
 
 
@@ -163,6 +186,23 @@ def _declare(lib):
     lib.usw_encode_device_values.restype = c_i32
     lib.usw_encode_device_values.argtypes = [c_vp, c_i32, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_i64, c_vp,
                                              c_sz, c_vp]
+    lib.usw_spmm_fused_workspace.restype = c_i32
+    lib.usw_spmm_fused_workspace.argtypes = [P(UswFmt), c_i32, c_i32, P(c_sz), P(c_sz)]
+    lib.usw_spmm_fused.restype = c_i32
+    lib.usw_spmm_fused.argtypes = [P(UswFmt), c_vp, c_vp, c_i32, c_i32, P(UswEpilogue), c_i32, c_vp, c_sz, c_vp]
+    lib.usw_expert_spmm_workspace.restype = c_i32
+    lib.usw_expert_spmm_workspace.argtypes = [P(UswExpertFmt), c_i32, P(c_sz), P(c_sz)]
+    lib.usw_expert_spmm.restype = c_i32
+    lib.usw_expert_spmm.argtypes = [P(UswExpertFmt), c_vp, c_i32, c_vp, c_vp, c_i32, c_vp, c_i32, P(UswEpilogue),
+                                    c_vp, c_sz, c_vp]
+    lib.usw_expert_route_workspace.restype = c_i32
+    lib.usw_expert_route_workspace.argtypes = [c_i32, c_i32, c_i32, P(c_sz)]
+    lib.usw_expert_route.restype = c_i32
+    lib.usw_expert_route.argtypes = [c_vp, c_i32, c_i64, c_i32, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                     c_vp, c_sz, c_vp]
+    lib.usw_expert_combine.restype = c_i32
+    lib.usw_expert_combine.argtypes = [c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_i64, c_vp, c_i32,
+                                       c_vp]
     return lib
 
 

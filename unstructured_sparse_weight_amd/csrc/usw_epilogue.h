@@ -1,0 +1,73 @@
+// The epilogue of the fused products: what happens to the fp32 sums of an
+// output tile before they are rounded and stored,
+//
+//   y[n][m] = res[n][m] + mul[n][m] * act(scale[m] * sum + bias[m]),
+//
+// each operand optional.  Everything is computed in fp32 on the sums where
+// the kernel already holds them, so the output is rounded once and neither
+// the pre-activation nor any intermediate reaches memory.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "usw.h"
+#include "usw_device.h"
+
+namespace usw_dev {
+
+struct Epilogue {
+  const uint16_t* __restrict__ bias;   // fp16 [M] or null
+  const uint16_t* __restrict__ mul;    // fp16 [rows][ld_mul] or null
+  const uint16_t* __restrict__ res;    // fp16 [rows][ld_res] or null
+  int64_t ld_mul, ld_res;
+  int act;                             // usw_act
+  int f16out;                          // y is fp16, else fp32
+};
+
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+
+// GELU's tanh form is v times the logistic function of 2z, z = sqrt(2/pi)
+// (v + 0.044715 v^3), because (1 + tanh z) / 2 = 1 / (1 + exp(-2z)).  For
+// very negative v the exponential overflows to infinity and the quotient is
+// the limit, -0.  ReLU keeps NaN.
+__device__ __forceinline__ float activate(float v, int act) {
+  switch (act) {
+    case USW_ACT_RELU: return v < 0.0f ? 0.0f : v;
+    case USW_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    case USW_ACT_GELU_TANH: return v / (1.0f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
+    case USW_ACT_SILU: return v / (1.0f + __expf(-v));
+    default: return v;
+  }
+}
+
+__device__ __forceinline__ f32x4_t load_half4(const uint16_t* p) {
+  const half4_t h = *reinterpret_cast<const half4_t*>(p);
+  return f32x4_t{static_cast<float>(h.x), static_cast<float>(h.y), static_cast<float>(h.z), static_cast<float>(h.w)};
+}
+
+// Applies the epilogue to the sums of row n, outputs m .. m+3 (m a multiple
+// of 4), and stores them at y + n M + m.
+__device__ __forceinline__ void epilogue_store4(const Epilogue& e, void* y, int M, int64_t n, int m, f32x4_t v) {
+  if (e.bias) v += load_half4(e.bias + m);
+  if (e.act != USW_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = activate(v[j], e.act);
+  }
+  if (e.mul) v *= load_half4(e.mul + n * e.ld_mul + m);
+  if (e.res) v += load_half4(e.res + n * e.ld_res + m);
+  const int64_t yi = n * M + m;
+  if (e.f16out) {
+    half4_t h;
+    h.x = static_cast<_Float16>(v.x);
+    h.y = static_cast<_Float16>(v.y);
+    h.z = static_cast<_Float16>(v.z);
+    h.w = static_cast<_Float16>(v.w);
+    *reinterpret_cast<half4_t*>(static_cast<_Float16*>(y) + yi) = h;
+  } else {
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(y) + yi) = v;
+  }
+}
+
+}  // namespace usw_dev

@@ -1,0 +1,266 @@
+// The sparse product with an epilogue, of one weight (usw_spmm_fused) and of
+// E expert weights over ragged runs of rows (usw_expert_spmm):
+//
+//   y[n][m] = res[n][m] + mul[n][m] * act(sum_k W_sp[m][k] x[n][k] + bias[m]).
+//
+// Few rows run on the decode kernels (usw_decode_kernels.h), instantiated
+// with arguments that carry the epilogue: it costs no launch and no pass over
+// memory, since it works on the fp32 sums a strip's last workgroup holds.
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "usw.h"
+#include "usw_decode_plan.h"
+#include "usw_internal.h"
+
+namespace {
+
+using namespace usw_dev;
+
+constexpr int kMaxExperts = 1024;
+
+// Checks an epilogue for rows of M outputs and fills the kernels' copy.
+usw_status make_epilogue(const usw_epilogue* ep, int64_t M, int32_t y_type, Epilogue* e) {
+  *e = Epilogue{nullptr, nullptr, nullptr, M, M, USW_ACT_NONE, y_type == USW_OUT_F16 ? 1 : 0};
+  if (!ep) return USW_OK;
+  if (ep->act < USW_ACT_NONE || ep->act > USW_ACT_SILU) return USW_ERR_BAD_DTYPE;
+  if (ep->reserved != 0) return USW_ERR_BAD_SHAPE;
+  e->act = ep->act;
+  e->bias = ep->bias;
+  e->mul = ep->mul;
+  e->res = ep->res;
+  if (ep->mul && ep->ld_mul != 0) e->ld_mul = ep->ld_mul;
+  if (ep->res && ep->ld_res != 0) e->ld_res = ep->ld_res;
+  constexpr int64_t kMaxLd = int64_t(1) << 31;
+  if (e->ld_mul < M || e->ld_res < M || e->ld_mul > kMaxLd || e->ld_res > kMaxLd) return USW_ERR_BAD_SHAPE;
+  if (!aligned16(ep->bias) || !aligned16(ep->mul) || !aligned16(ep->res) || e->ld_mul % 8 || e->ld_res % 8)
+    return USW_ERR_MISALIGNED;
+  return USW_OK;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// ---------------------------------------------------------------------------
+// One weight
+// ---------------------------------------------------------------------------
+
+struct FusedPlan {
+  Plan p;
+  size_t need, cb;
+};
+
+FusedPlan plan_fused(const usw_fmt* f, const usw::Geometry& g, int32_t N, int splits_req) {
+  FusedPlan c{};
+  c.p = make_plan<FusedArgs>(g, N, splits_req, f->val_type == USW_VAL_I4, lean_values(f, g));
+  c.need = workspace_bytes(g, c.p);
+  c.cb = c.need > 0 ? counters_bytes(g) : 0;
+  return c;
+}
+
+usw_status fused_impl(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_type, int32_t N, const usw_epilogue* ep,
+                      int splits_req, void* ws, size_t ws_bytes, void* stream) {
+  usw::Geometry g;
+  usw_status st = check_common(f, y_type, N, &g);
+  if (st) return st;
+  if (!X || !Y || !f->bitmaps || !f->offsets || !f->values) return USW_ERR_NULL_ARG;
+  const bool i4 = f->val_type == USW_VAL_I4;
+  if (i4 && !f->scales) return USW_ERR_NULL_ARG;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(f->bitmaps) || !aligned16(f->values) ||
+      (reinterpret_cast<uintptr_t>(f->offsets) & 3u) || (i4 && !aligned16(f->scales)))
+    return USW_ERR_MISALIGNED;
+  Epilogue e;
+  st = make_epilogue(ep, g.M, y_type, &e);
+  if (st) return st;
+  const FusedPlan c = plan_fused(f, g, N, splits_req);
+  if (c.need > 0) {
+    if (!ws || ws_bytes < c.need) return USW_ERR_WORKSPACE;
+    if (!aligned16(ws)) return USW_ERR_MISALIGNED;
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const Plan& p = c.p;
+  const bool lean = lean_values(f, g);
+  for (int n0 = 0; n0 < N; n0 += p.nchunk) {
+    const int nc = std::min(p.nchunk, N - n0);
+    const int splits = (p.rchunk > 0 && n0 + p.nchunk > N) ? p.rsplits : p.splits;
+    const int64_t nblk = g.Gr * splits;
+    FusedArgs a{};
+    a.bitmaps = f->bitmaps;
+    a.offsets = f->offsets;
+    a.values = static_cast<const uint8_t*>(f->values);
+    a.scales = i4 ? f->scales : nullptr;
+    a.X = X + static_cast<size_t>(n0) * g.K;
+    a.Y = static_cast<uint8_t*>(Y) + static_cast<size_t>(n0) * g.M * (e.f16out ? 2 : 4);
+    if (c.need) {
+      a.counters = static_cast<uint32_t*>(ws);
+      a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + c.cb);
+    }
+    a.values_alloc = usw::values_alloc_bytes(f->val_type, f->nnz);
+    a.M = static_cast<int>(g.M);
+    a.K = static_cast<int>(g.K);
+    a.N = nc;
+    a.Gc = static_cast<int>(g.Gc);
+    a.splits = splits;
+    a.remap = (splits > 1 && nblk % 8 == 0) ? 1 : 0;
+    a.e = e;
+    if (e.mul) a.e.mul += e.ld_mul * n0;
+    if (e.res) a.e.res += e.ld_res * n0;
+    const int nb = nc > 32 ? 4 : nc > 16 ? 2 : 1;
+    launch_pass(a, p.ring, i4, lean, nb, true, dim3(static_cast<unsigned>(nblk)), s);
+    if (hipGetLastError() != hipSuccess) return USW_ERR_HIP;
+  }
+  return USW_OK;
+}
+
+// ---------------------------------------------------------------------------
+// By expert
+// ---------------------------------------------------------------------------
+
+struct ExpertPlan {
+  int lg_chunk;      // slots per tile: 16, 32 or 64
+  int64_t tiles;     // most tiles the slots can make
+  int splits;        // workgroups per tile and 64-row strip
+  bool ring, lean;
+  size_t need, cb;
+};
+
+usw_status check_expert(const usw_expert_fmt* f, int32_t y_type, int32_t S, usw::Geometry* g) {
+  if (!f) return USW_ERR_NULL_ARG;
+  usw_status st = usw::make_geometry(f->M, f->K, kGT, kGT, g);
+  if (st) return st;
+  if (f->E < 1 || f->reserved != 0) return USW_ERR_BAD_SHAPE;
+  if (f->E > kMaxExperts) return USW_ERR_UNSUPPORTED;
+  if (f->val_type != USW_VAL_F16 && f->val_type != USW_VAL_I4) return USW_ERR_BAD_DTYPE;
+  if (y_type != USW_OUT_F16 && y_type != USW_OUT_F32) return USW_ERR_BAD_DTYPE;
+  if (S < 0) return USW_ERR_BAD_N;
+  if (f->nnz < 0 || f->nnz > f->E * g->M * g->K || f->values_bytes < 16 * int64_t(f->E) || f->values_bytes % 16)
+    return USW_ERR_BAD_SHAPE;
+  if (static_cast<int64_t>(S) * g->M > (int64_t(1) << 40)) return USW_ERR_BAD_SHAPE;
+  return USW_OK;
+}
+
+ExpertPlan plan_expert(const usw_expert_fmt* f, const usw::Geometry& g, int32_t S) {
+  ExpertPlan p{};
+  const bool i4 = f->val_type == USW_VAL_I4;
+  p.lean = !i4 && static_cast<double>(f->nnz) <= 0.55 * static_cast<double>(f->E) * g.M * g.K;
+  const int64_t active = std::min<int64_t>(f->E, S);
+  const int64_t mean = S / std::max<int64_t>(1, active);
+  p.lg_chunk = mean <= 8 ? 4 : mean <= 24 ? 5 : 6;
+  const int chunk = 1 << p.lg_chunk;
+  p.tiles = active + (S - active) / chunk;
+  p.ring = p.lean && chunk == 16;
+  // One round of resident workgroups over the tiles, as the plain product
+  // splits a matrix with that many strips.
+  usw::Geometry gt = g;
+  gt.Gr = g.Gr * p.tiles;
+  const Plan one = make_plan<ExpertArgs>(gt, chunk, 0, i4, p.lean);
+  p.splits = one.splits;
+  if (p.splits > 1) {
+    p.cb = align256(static_cast<size_t>(4) * p.tiles * g.Gr);
+    p.need = p.cb + static_cast<size_t>(p.splits) * S * g.M * sizeof(float);
+  }
+  return p;
+}
+
+usw_status expert_impl(const usw_expert_fmt* f, const uint16_t* X, int32_t T, const int32_t* slots,
+                       const int32_t* rows, int32_t S, void* Y, int32_t y_type, const usw_epilogue* ep, void* ws,
+                       size_t ws_bytes, void* stream) {
+  usw::Geometry g;
+  usw_status st = check_expert(f, y_type, S, &g);
+  if (st) return st;
+  const bool i4 = f->val_type == USW_VAL_I4;
+  if (T < 0 || (!rows && T < S) || (S > 0 && T == 0)) return USW_ERR_BAD_N;
+  if (!f->bitmaps || !f->offsets || !f->values || !f->starts || (i4 && !f->scales) || !slots) return USW_ERR_NULL_ARG;
+  if (S > 0 && (!X || !Y)) return USW_ERR_NULL_ARG;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(f->bitmaps) || !aligned16(f->values) ||
+      ((reinterpret_cast<uintptr_t>(f->offsets) | reinterpret_cast<uintptr_t>(slots) |
+        reinterpret_cast<uintptr_t>(rows)) & 3u) ||
+      (reinterpret_cast<uintptr_t>(f->starts) & 7u) || (i4 && !aligned16(f->scales)))
+    return USW_ERR_MISALIGNED;
+  Epilogue e;
+  st = make_epilogue(ep, g.M, y_type, &e);
+  if (st) return st;
+  if (S == 0) return USW_OK;
+  const ExpertPlan p = plan_expert(f, g, S);
+  if (p.need > 0) {
+    if (!ws || ws_bytes < p.need) return USW_ERR_WORKSPACE;
+    if (!aligned16(ws)) return USW_ERR_MISALIGNED;
+  }
+  const int64_t per = g.Gr * p.splits;
+  if (p.tiles * per >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
+  ExpertArgs a{};
+  a.bitmaps = f->bitmaps;
+  a.offsets = f->offsets;
+  a.values = static_cast<const uint8_t*>(f->values);
+  a.scales = i4 ? f->scales : nullptr;
+  a.X = X;
+  a.Y = Y;
+  if (p.need) {
+    a.counters = static_cast<uint32_t*>(ws);
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.cb);
+  }
+  a.M = static_cast<int>(g.M);
+  a.K = static_cast<int>(g.K);
+  a.Gc = static_cast<int>(g.Gc);
+  a.splits = p.splits;
+  a.remap = per % 8 == 0 ? 1 : 0;
+  a.e = e;
+  a.slots = slots;
+  a.rows = rows;
+  a.starts = f->starts;
+  a.values_total = f->values_bytes;
+  a.nbt = g.nbt;
+  a.noff = g.ngt + 1;
+  a.E = f->E;
+  a.S = S;
+  a.T = T;
+  a.tiles = static_cast<int>(p.tiles);
+  a.lg_chunk = p.lg_chunk;
+  a.Gr = static_cast<int>(g.Gr);
+  launch_pass(a, p.ring, i4, p.lean, 1 << (p.lg_chunk - 4), true, dim3(static_cast<unsigned>(p.tiles * per)),
+              static_cast<hipStream_t>(stream));
+  return hipGetLastError() == hipSuccess ? USW_OK : USW_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+usw_status usw_spmm_fused_workspace(const usw_fmt* f, int32_t N, int32_t splits, size_t* bytes, size_t* counter_bytes) {
+  if (!bytes || !counter_bytes) return USW_ERR_NULL_ARG;
+  usw::Geometry g;
+  usw_status st = check_common(f, USW_OUT_F16, N, &g);
+  if (st) return st;
+  const FusedPlan c = plan_fused(f, g, N, splits < 0 ? 0 : splits);
+  *bytes = c.need;
+  *counter_bytes = c.cb;
+  return USW_OK;
+}
+
+usw_status usw_spmm_fused(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_type, int32_t N,
+                          const usw_epilogue* ep, int32_t splits, void* ws, size_t ws_bytes, void* stream) {
+  return fused_impl(f, X, Y, y_type, N, ep, splits < 0 ? 0 : splits, ws, ws_bytes, stream);
+}
+
+usw_status usw_expert_spmm_workspace(const usw_expert_fmt* f, int32_t S, size_t* bytes, size_t* counter_bytes) {
+  if (!bytes || !counter_bytes) return USW_ERR_NULL_ARG;
+  usw::Geometry g;
+  usw_status st = check_expert(f, USW_OUT_F16, S, &g);
+  if (st) return st;
+  *bytes = *counter_bytes = 0;
+  if (S == 0) return USW_OK;
+  const ExpertPlan p = plan_expert(f, g, S);
+  *bytes = p.need;
+  *counter_bytes = p.cb;
+  return USW_OK;
+}
+
+usw_status usw_expert_spmm(const usw_expert_fmt* f, const uint16_t* X, int32_t T, const int32_t* slots,
+                           const int32_t* rows, int32_t S, void* Y, int32_t y_type, const usw_epilogue* ep, void* ws,
+                           size_t ws_bytes, void* stream) {
+  return expert_impl(f, X, T, slots, rows, S, Y, y_type, ep, ws, ws_bytes, stream);
+}
+
+}  // extern "C"
