@@ -6,6 +6,7 @@
 // Few rows run on the decode kernels (usw_decode_kernels.h), instantiated
 // with arguments that carry the epilogue: it costs no launch and no pass over
 // memory, since it works on the fp32 sums a strip's last workgroup holds.
+// Many rows run on the expanded weight (usw_wide.hip).
 
 #include <hip/hip_runtime.h>
 
@@ -15,6 +16,7 @@
 #include "usw.h"
 #include "usw_decode_plan.h"
 #include "usw_internal.h"
+#include "usw_wide.h"
 
 namespace {
 
@@ -48,12 +50,24 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // ---------------------------------------------------------------------------
 
 struct FusedPlan {
-  Plan p;
+  bool wide;
+  Plan p;               // decode passes
+  usw::WidePlan w;
   size_t need, cb;
 };
 
+// Rows from which the weight is expanded.
+constexpr int kWideMinRows = 160;
+
 FusedPlan plan_fused(const usw_fmt* f, const usw::Geometry& g, int32_t N, int splits_req) {
   FusedPlan c{};
+  c.wide = N >= kWideMinRows && splits_req <= 0;
+  if (c.wide) {
+    c.w = usw::wide_plan(g, 1, N);
+    c.need = c.w.need;
+    c.cb = c.w.cb;
+    return c;
+  }
   c.p = make_plan<FusedArgs>(g, N, splits_req, f->val_type == USW_VAL_I4, lean_values(f, g));
   c.need = workspace_bytes(g, c.p);
   c.cb = c.need > 0 ? counters_bytes(g) : 0;
@@ -78,6 +92,21 @@ usw_status fused_impl(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_ty
   if (c.need > 0) {
     if (!ws || ws_bytes < c.need) return USW_ERR_WORKSPACE;
     if (!aligned16(ws)) return USW_ERR_MISALIGNED;
+  }
+  if (c.wide) {
+    usw::WideCall w{};
+    w.bitmaps = f->bitmaps;
+    w.offsets = f->offsets;
+    w.values = static_cast<const uint8_t*>(f->values);
+    w.scales = f->scales;
+    w.values_total = static_cast<int64_t>(usw::values_alloc_bytes(f->val_type, f->nnz));
+    w.val_type = f->val_type;
+    w.E = 1;
+    w.X = X;
+    w.S = w.T = N;
+    w.Y = Y;
+    w.e = e;
+    return usw::wide_launch(w, g, c.w, ws, stream);
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   const Plan& p = c.p;
@@ -119,6 +148,8 @@ usw_status fused_impl(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_ty
 // ---------------------------------------------------------------------------
 
 struct ExpertPlan {
+  bool wide;
+  usw::WidePlan w;
   int lg_chunk;      // slots per tile: 16, 32 or 64
   int64_t tiles;     // most tiles the slots can make
   int splits;        // workgroups per tile and 64-row strip
@@ -141,12 +172,22 @@ usw_status check_expert(const usw_expert_fmt* f, int32_t y_type, int32_t S, usw:
   return USW_OK;
 }
 
+// Rows per expert, on average, from which the weights are expanded.
+constexpr int kWideMinMean = 100;
+
 ExpertPlan plan_expert(const usw_expert_fmt* f, const usw::Geometry& g, int32_t S) {
   ExpertPlan p{};
   const bool i4 = f->val_type == USW_VAL_I4;
   p.lean = !i4 && static_cast<double>(f->nnz) <= 0.55 * static_cast<double>(f->E) * g.M * g.K;
   const int64_t active = std::min<int64_t>(f->E, S);
   const int64_t mean = S / std::max<int64_t>(1, active);
+  p.wide = mean >= kWideMinMean;
+  if (p.wide) {
+    p.w = usw::wide_plan(g, f->E, S);
+    p.need = p.w.need;
+    p.cb = p.w.cb;
+    return p;
+  }
   p.lg_chunk = mean <= 8 ? 4 : mean <= 24 ? 5 : 6;
   const int chunk = 1 << p.lg_chunk;
   p.tiles = active + (S - active) / chunk;
@@ -187,6 +228,25 @@ usw_status expert_impl(const usw_expert_fmt* f, const uint16_t* X, int32_t T, co
   if (p.need > 0) {
     if (!ws || ws_bytes < p.need) return USW_ERR_WORKSPACE;
     if (!aligned16(ws)) return USW_ERR_MISALIGNED;
+  }
+  if (p.wide) {
+    usw::WideCall w{};
+    w.bitmaps = f->bitmaps;
+    w.offsets = f->offsets;
+    w.values = static_cast<const uint8_t*>(f->values);
+    w.starts = f->starts;
+    w.scales = f->scales;
+    w.values_total = f->values_bytes;
+    w.val_type = f->val_type;
+    w.E = f->E;
+    w.X = X;
+    w.slots = slots;
+    w.rows = rows;
+    w.S = S;
+    w.T = T;
+    w.Y = Y;
+    w.e = e;
+    return usw::wide_launch(w, g, p.w, ws, stream);
   }
   const int64_t per = g.Gr * p.splits;
   if (p.tiles * per >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
