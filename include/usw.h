@@ -661,12 +661,15 @@ usw_status usw_spmm_fused_workspace(const usw_fmt* fmt, int32_t N, int32_t split
 
 /*
  * Y [N][M] as above, X [N][K] fp16.  As usw_spmm_ex otherwise (layouts,
- * alignment, splits, workspace, stream, determinism).  ep may be NULL: no
+ * alignment, splits, workspace, stream, determinism).  Few rows take the
+ * decode kernels in passes of up to 64; from 65 rows (large fp16 weights: 129
+ * or 193) the weight is expanded once to dense fp16 in the workspace (2 M K
+ * bytes) and multiplied there, unless splits > 0.  ep may be NULL: no
  * epilogue.  ep and the struct it points to are read during the call.  Y may
  * be the residual itself (same address, ld_res = M); it may overlap nothing
  * else that the call reads.
  * Errors: as usw_spmm_ex, and BAD_DTYPE (act), BAD_SHAPE (a stride below M or
- * above 2^31, reserved), MISALIGNED (scales, bias, mul or res not 16-byte
+ * above 2^20, reserved), MISALIGNED (scales, bias, mul or res not 16-byte
  * aligned, a stride that is no multiple of 8).
  */
 usw_status usw_spmm_fused(const usw_fmt* fmt, const uint16_t* X, void* Y, int32_t y_type, int32_t N,
@@ -687,6 +690,9 @@ typedef struct usw_expert_fmt {
   const uint16_t* scales;   /* I4: fp16 [E][M]; F16: ignored */
 } usw_expert_fmt;
 
+/* Workspace of usw_expert_spmm for S slots, with usw_spmm_fused_workspace's
+ * rules.  With 128 slots an expert or more it holds expanded weights, up to
+ * 1 GiB of them (or one) at a time. */
 usw_status usw_expert_spmm_workspace(const usw_expert_fmt* fmt, int32_t S, size_t* bytes, size_t* counter_bytes);
 
 /*

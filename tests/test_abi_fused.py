@@ -45,7 +45,7 @@ def fused(f=None, X=P, Y=P, yt=1, N=4, e=None, splits=1, ws=None, ws_bytes=0):
     (BAD_DTYPE, dict(e=ep(act=5))), (BAD_DTYPE, dict(e=ep(act=-1))), (BAD_SHAPE, dict(e=ep(reserved=1))),
     (MISALIGNED, dict(e=ep(bias=P + 8))), (MISALIGNED, dict(e=ep(mul=P + 2))), (MISALIGNED, dict(e=ep(res=P + 8))),
     (BAD_SHAPE, dict(e=ep(mul=P, ld_mul=M - 8))), (BAD_SHAPE, dict(e=ep(res=P, ld_res=-8))),
-    (MISALIGNED, dict(e=ep(res=P, ld_res=M + 4))), (BAD_SHAPE, dict(e=ep(mul=P, ld_mul=(1 << 31) + 8))),
+    (MISALIGNED, dict(e=ep(res=P, ld_res=M + 4))), (BAD_SHAPE, dict(e=ep(mul=P, ld_mul=(1 << 20) + 8))),
 ])
 def test_fused_refuses(want, kw):
     assert fused(**kw) == want

@@ -136,6 +136,35 @@ def test_integer_exact_is_bitwise(val, density, counts):
     assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
 
 
+# Expanded weights: small, medium and large tiles, runs that end inside tiles,
+# and experts without rows (whose weights are not expanded).
+EXPANDED = [([200, 0, 320, 131], 192, 320, "small"), ([500, 900, 0, 700], 1280, 1664, "medium"),
+            ([2100, 100, 1900, 0, 2300], 2112, 128, "small, many"), ([2100, 100, 1900, 0, 2300], 2496, 192, "large")]
+
+
+@pytest.mark.parametrize("counts,M,K,what", EXPANDED, ids=[e[3] for e in EXPANDED])
+@pytest.mark.parametrize("val", ["f16", "i4"])
+def test_expanded_tilings(counts, M, K, what, val):
+    E = len(counts)
+    bank, dense, scales = bank_of(E, M, K, val, 100 + M)
+    slots = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    live = int(slots[-1])
+    S = live + 7
+    rng = np.random.default_rng(101)
+    T = 1000
+    rows = rng.integers(0, T, size=S).astype(np.int32)
+    rows[live:] = -1
+    x, bias = half(rng, T, K), half(rng, E, M)
+    say(f"[experts] expanded {what} {val}")
+    y = torch.full((S, M), 7.0, dtype=torch.float16, device=DEV)
+    usw.expert_spmm(bank, gpu(x), gpu(slots), rows=gpu(rows), bias=gpu(bias), act="relu", y=y)
+    assert torch.all(y[live:] == 7.0)
+    z = usw.expert_spmm(bank, gpu(x), gpu(slots), rows=gpu(rows), bias=gpu(bias), act="relu")
+    assert torch.equal(y[:live], z[:live])
+    want, bound = runs_reference(dense, scales, x, slots, rows, bias, "relu", None, "f16")
+    near(y, want, bound, what)
+
+
 def test_long_rows_split_k_twice_the_same():
     """Few slots and long rows: several workgroups a strip; two calls give the
     same bits."""

@@ -155,6 +155,38 @@ def test_split_factors(splits, val, N):
     near(y, want, bound, "splits")
 
 
+# Every tiling of the expanded product: small tiles with and without splits,
+# medium ones with and without, large ones with tiles left over after the
+# whole rounds; outputs and rows that end inside a tile.
+EXPANDED = [(320, 1024, 70, "small, split"), (1600, 512, 700, "small"), (1088, 2112, 1900, "medium, split"),
+            (2624, 832, 2050, "medium"), (4160, 192, 4200, "large"), (4096, 64, 4096, "large, one column")]
+
+
+@pytest.mark.parametrize("M,K,N,what", EXPANDED, ids=[e[3] for e in EXPANDED])
+@pytest.mark.parametrize("val", ["f16", "i4"])
+def test_expanded_tilings(M, K, N, what, val):
+    enc, Wd, scale = weight(M, K, 0.5, val, 300 + N)
+    rng = np.random.default_rng(301)
+    x, b, mul = half(rng, N, K), half(rng, M), half(rng, N, M)
+    say(f"[fused] expanded {what} {val}")
+    y = usw.spmm_fused(enc, gpu(x), bias=gpu(b), act="relu", mul=gpu(mul))
+    assert torch.equal(y, usw.spmm_fused(enc, gpu(x), bias=gpu(b), act="relu", mul=gpu(mul)))
+    want, bound = ref.product(Wd, x, b, "relu", mul, None, "f16", scale)
+    near(y, want, bound, what)
+
+
+@pytest.mark.parametrize("M,K,N,what", EXPANDED, ids=[e[3] for e in EXPANDED])
+def test_expanded_is_exact_on_integers(M, K, N, what):
+    enc, Wd, _ = weight(M, K, 0.6, "f16", 310 + N, exact=True)
+    rng = np.random.default_rng(311)
+    x = wl.activations_small_int(N, K, rng)
+    res = rng.integers(-8, 9, size=(N, M)).astype(np.float16)
+    say(f"[fused] expanded exact {what}")
+    y = usw.spmm_fused(enc, gpu(x), residual=gpu(res), out_dtype=torch.float32)
+    want = x.astype(np.float64) @ Wd.T + res.astype(np.float64)
+    assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
+
+
 def test_relu_and_large_values():
     """Sums far out: ReLU keeps zeros, SiLU and GELU go to 0 and to v, and an
     fp16 result past the range is an infinity."""

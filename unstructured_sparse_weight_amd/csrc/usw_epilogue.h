@@ -32,19 +32,47 @@ typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 // (v + 0.044715 v^3), because (1 + tanh z) / 2 = 1 / (1 + exp(-2z)).  For
 // very negative v the exponential overflows to infinity and the quotient is
 // the limit, -0.  ReLU keeps NaN.
+template <int ACT>
+__device__ __forceinline__ float activation(float v) {
+  if constexpr (ACT == USW_ACT_RELU) return v < 0.0f ? 0.0f : v;
+  else if constexpr (ACT == USW_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  else if constexpr (ACT == USW_ACT_GELU_TANH)
+    return v / (1.0f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
+  else if constexpr (ACT == USW_ACT_SILU) return v / (1.0f + __expf(-v));
+  else return v;
+}
+
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
-    case USW_ACT_RELU: return v < 0.0f ? 0.0f : v;
-    case USW_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    case USW_ACT_GELU_TANH: return v / (1.0f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
-    case USW_ACT_SILU: return v / (1.0f + __expf(-v));
+    case USW_ACT_RELU: return activation<USW_ACT_RELU>(v);
+    case USW_ACT_GELU: return activation<USW_ACT_GELU>(v);
+    case USW_ACT_GELU_TANH: return activation<USW_ACT_GELU_TANH>(v);
+    case USW_ACT_SILU: return activation<USW_ACT_SILU>(v);
     default: return v;
   }
 }
 
-__device__ __forceinline__ f32x4_t load_half4(const uint16_t* p) {
-  const half4_t h = *reinterpret_cast<const half4_t*>(p);
+__device__ __forceinline__ f32x4_t to_float4(half4_t h) {
   return f32x4_t{static_cast<float>(h.x), static_cast<float>(h.y), static_cast<float>(h.z), static_cast<float>(h.w)};
+}
+__device__ __forceinline__ f32x4_t load_half4(const uint16_t* p) { return to_float4(*reinterpret_cast<const half4_t*>(p)); }
+
+__device__ __forceinline__ half4_t to_half4(f32x4_t v) {
+  half4_t h;
+  h.x = static_cast<_Float16>(v.x);
+  h.y = static_cast<_Float16>(v.y);
+  h.z = static_cast<_Float16>(v.z);
+  h.w = static_cast<_Float16>(v.w);
+  return h;
+}
+
+// Stores four outputs, rounded to y's type, at y + at.
+__device__ __forceinline__ void store_out4(void* y, int64_t at, int f16out, f32x4_t v) {
+  if (f16out) {
+    *reinterpret_cast<half4_t*>(static_cast<_Float16*>(y) + at) = to_half4(v);
+  } else {
+    *reinterpret_cast<f32x4_t*>(static_cast<float*>(y) + at) = v;
+  }
 }
 
 // Applies the epilogue to the sums of row n, outputs m .. m+3 (m a multiple
@@ -57,17 +85,7 @@ __device__ __forceinline__ void epilogue_store4(const Epilogue& e, void* y, int 
   }
   if (e.mul) v *= load_half4(e.mul + n * e.ld_mul + m);
   if (e.res) v += load_half4(e.res + n * e.ld_res + m);
-  const int64_t yi = n * M + m;
-  if (e.f16out) {
-    half4_t h;
-    h.x = static_cast<_Float16>(v.x);
-    h.y = static_cast<_Float16>(v.y);
-    h.z = static_cast<_Float16>(v.z);
-    h.w = static_cast<_Float16>(v.w);
-    *reinterpret_cast<half4_t*>(static_cast<_Float16*>(y) + yi) = h;
-  } else {
-    *reinterpret_cast<f32x4_t*>(static_cast<float*>(y) + yi) = v;
-  }
+  store_out4(y, n * M + m, e.f16out, v);
 }
 
 }  // namespace usw_dev

@@ -23,6 +23,9 @@ namespace {
 using namespace usw_dev;
 
 constexpr int kMaxExperts = 1024;
+// Longest stride of the epilogue's operands, and most outputs of an expanded
+// weight: the expanded product addresses a tile's rows with 32 bits.
+constexpr int64_t kMaxLd = int64_t(1) << 20;
 
 // Checks an epilogue for rows of M outputs and fills the kernels' copy.
 usw_status make_epilogue(const usw_epilogue* ep, int64_t M, int32_t y_type, Epilogue* e) {
@@ -36,8 +39,8 @@ usw_status make_epilogue(const usw_epilogue* ep, int64_t M, int32_t y_type, Epil
   e->res = ep->res;
   if (ep->mul && ep->ld_mul != 0) e->ld_mul = ep->ld_mul;
   if (ep->res && ep->ld_res != 0) e->ld_res = ep->ld_res;
-  constexpr int64_t kMaxLd = int64_t(1) << 31;
-  if (e->ld_mul < M || e->ld_res < M || e->ld_mul > kMaxLd || e->ld_res > kMaxLd) return USW_ERR_BAD_SHAPE;
+  if (e->ld_mul < M || e->ld_res < M || (ep->mul && e->ld_mul > kMaxLd) || (ep->res && e->ld_res > kMaxLd))
+    return USW_ERR_BAD_SHAPE;
   if (!aligned16(ep->bias) || !aligned16(ep->mul) || !aligned16(ep->res) || e->ld_mul % 8 || e->ld_res % 8)
     return USW_ERR_MISALIGNED;
   return USW_OK;
@@ -56,12 +59,27 @@ struct FusedPlan {
   size_t need, cb;
 };
 
-// Rows from which the weight is expanded.
-constexpr int kWideMinRows = 160;
+bool fits_wide(const usw::Geometry& g) { return g.M <= kMaxLd; }
+
+// Rows from which the weight is expanded; fewer take passes of up to 64 rows
+// that rebuild it each time.  Two passes cost as much as the expansion and
+// the product on weights of about 2^24 elements and on all INT4 weights,
+// whose expansion reads less (MI355X, passes / expanded: 1152x1152 N = 80
+// 20.6 / 12.5 us, 4096x4096 N = 70 26.5 / 27.6 and N = 100 28.5 / 26.2, INT4
+// 20480x5120 N = 128 105 / 88); on larger ones three (11008x4096 N = 96 45.9
+// / 48.5, N = 128 51.9 / 50.1), on the largest four (20480x5120 N = 160 137 /
+// 148, N = 200 165 / 160).  A caller's split factor asks for the passes.
+bool use_wide(const usw_fmt* f, const usw::Geometry& g, int32_t N, int splits_req) {
+  const int64_t elements = g.M * g.K;
+  const int from = f->val_type == USW_VAL_I4 || elements <= (int64_t(1) << 24) ? 64
+                   : elements <= (int64_t(1) << 26)                            ? 128
+                                                                               : 192;
+  return N > from && splits_req <= 0 && fits_wide(g);
+}
 
 FusedPlan plan_fused(const usw_fmt* f, const usw::Geometry& g, int32_t N, int splits_req) {
   FusedPlan c{};
-  c.wide = N >= kWideMinRows && splits_req <= 0;
+  c.wide = use_wide(f, g, N, splits_req);
   if (c.wide) {
     c.w = usw::wide_plan(g, 1, N);
     c.need = c.w.need;
@@ -172,16 +190,18 @@ usw_status check_expert(const usw_expert_fmt* f, int32_t y_type, int32_t S, usw:
   return USW_OK;
 }
 
-// Rows per expert, on average, from which the weights are expanded.
-constexpr int kWideMinMean = 100;
-
 ExpertPlan plan_expert(const usw_expert_fmt* f, const usw::Geometry& g, int32_t S) {
   ExpertPlan p{};
   const bool i4 = f->val_type == USW_VAL_I4;
   p.lean = !i4 && static_cast<double>(f->nnz) <= 0.55 * static_cast<double>(f->E) * g.M * g.K;
   const int64_t active = std::min<int64_t>(f->E, S);
   const int64_t mean = S / std::max<int64_t>(1, active);
-  p.wide = mean >= kWideMinMean;
+  // Rows per expert from which expanding pays (MI355X, fp16): with weights of
+  // up to 2^26 elements in all, where the passes leave compute units idle,
+  // 128 (8 experts of 2048x2048: 43.9 us in passes, 42.9 expanded; 16 of
+  // 2048x1024, 250 rows each: 69.8 / 50.9); above, 224 (8 of 11008x4096, 200
+  // rows each: 428 / 481; 8 of 4096x11008, 500 rows each: 800 / 684).
+  p.wide = mean >= (f->E * g.M * g.K <= (int64_t(1) << 26) ? 128 : 224) && fits_wide(g);
   if (p.wide) {
     p.w = usw::wide_plan(g, f->E, S);
     p.need = p.w.need;

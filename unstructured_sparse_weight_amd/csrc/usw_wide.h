@@ -31,9 +31,10 @@ struct WideCall {
 
 struct WidePlan {
   int group;        // weights expanded and multiplied at a time
+  int tiling;       // 0, 1, 2: large, medium, small tiles
+  int splits;       // workgroups that share a tile's columns
   int64_t tiles;    // most output tiles of one group
-  int wgs;          // workgroups of the product
-  size_t cb, slots_at, dense_at, need;   // workspace: counters, partial sums, dense fragments
+  size_t cb, dense_at, need;   // workspace: counters, partial sums, then the dense fragments
 };
 
 WidePlan wide_plan(const Geometry& g, int32_t E, int32_t S);

@@ -4,32 +4,33 @@
 //     core fragments in the workspace, once per call (INT4: the codes; the row
 //     scales go into the epilogue).  A wave takes a GroupTile, as in decode;
 //     it is bound by the bytes it writes, 2 per element.
-//  2. wide_kernel multiplies them: tiles of 256 outputs by 256 rows, eight
-//     waves of 128 x 64 each, fp32 accumulators in registers, both operands
-//     through LDS by LDS-DMA a GroupTile column ahead.
+//  2. wide_kernel multiplies them, fp32 accumulators in registers, both
+//     operands through LDS by LDS-DMA several half columns (32 k) ahead, the
+//     fragments of the next half column read between the MFMAs of this one.
 //
-// Rebuilding inside the product instead costs LDS time on every column for
-// every tile of rows, and LDS is what bounds the product: per column a wave
-// reads 16 KB of weight and 8 KB of x fragments for 64 MFMAs of 16 cycles,
-// 0.75 of the matrix time at 128 B a cycle, before any rebuild.
+// Rebuilding inside the product instead would cost LDS time on every column
+// for every tile of rows, and LDS is what the product is next bound by: per
+// column a wave of the large tiling reads 24 KB of fragments for 64 MFMAs of
+// 16 cycles, 0.75 of the matrix time at 128 B a cycle, before any rebuild.
+// The large tiling reaches 1180 TFLOP/s on 4096^3 (116 us; the library's dense
+// product 1350 on 8192^3), where the clock falls under load.
 //
 // Fragments in the workspace are in the order a wave reads them (1 KB each),
 // so their copies to LDS and the reads from it are contiguous.  Rows of x are
-// copied as they lie (eight lanes per 128-byte piece of a row, gathered rows
-// alike), the 16-byte pieces of row r rotated by xor with (r / 2) % 8, which
-// spreads a fragment's 16 rows over all banks.
+// copied as they lie, gathered rows alike.
 //
-// Work split: the tiles are dealt to one workgroup per compute unit, whole
-// rounds of tiles first; the GroupTile columns of the tiles left over are
+// Work split, large tiles: they are dealt to one workgroup per compute unit,
+// whole rounds of tiles; the GroupTile columns of the tiles left over are
 // split evenly (a tile may then be shared by workgroups, which leave fp32
 // partial sums; the last to finish adds them in column order, so results do
-// not depend on timing).  Consecutive tiles are up to eight tiles of rows by
-// the weight's strips, so the 32 workgroups of an XCD share both operands in
-// its L2.
+// not depend on timing).  Smaller tiles are a workgroup each, or a few that
+// split the columns.  Consecutive tiles are up to eight tiles of rows by the
+// weight's strips, so the workgroups of an XCD share both operands in its L2.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "usw.h"
 #include "usw_decode_kernels.h"
@@ -54,6 +55,15 @@ struct ExpandArgs {
   int64_t values_total, ngt;
   int e0, S;
 };
+
+// Waits until at most N of this wave's loads are in flight, then the barrier.
+template <int N>
+__device__ __forceinline__ void ring_barrier() {
+  static_assert(N == 2 || N == 4 || N == 8, "one case for each tiling");
+  if constexpr (N == 2) USW_PRODUCER_BARRIER(2);
+  else if constexpr (N == 4) USW_PRODUCER_BARRIER(4);
+  else USW_PRODUCER_BARRIER(8);
+}
 
 constexpr int kExpandWaves = 4;
 
@@ -127,13 +137,28 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(ExpandArgs a)
 // Product
 // ---------------------------------------------------------------------------
 
-constexpr int kWideM = 256, kWideN = 256;
-constexpr int kWideThreads = 512;
-constexpr int kWideSlot = kWideM * kWideN;   // fp32 partial sums of a tile
-constexpr int64_t kComputeUnits = 256;
-// Fewest GroupTile columns of a split tile's piece: shorter ones cost more in
-// partial sums than the workgroup's share of the columns.
-constexpr int kWideMinCols = 16;
+// Fewest columns of a streaming workgroup's share: shorter ones cost more in
+// partial sums than they save.
+constexpr int kStreamMinCols = 16;
+
+// A tile is BM outputs by BN rows: WM x WN waves of 16 MF outputs by 16 NF
+// rows, and an LDS ring of RING half columns (32 k).  STREAM: the tiles are
+// dealt to one workgroup per compute unit and the rest's columns shared;
+// otherwise every tile, or equal share of its columns, is a workgroup.
+template <int MF_, int NF_, int WM_, int WN_, int RING_, bool STREAM_>
+struct Tiling {
+  static constexpr int MF = MF_, NF = NF_, WM = WM_, WN = WN_;
+  static constexpr bool kStream = STREAM_;
+  static constexpr int W = WM * WN, kThreads = 64 * W;
+  static constexpr int BM = 16 * MF * WM, BN = 16 * NF * WN;
+  static constexpr int kA = BM / 16, kB = BN / 16;      // 1 KB loads of a half column
+  static constexpr int kLoads = (kA + kB) / W;           // of them a wave issues
+  static constexpr int kPlace = 1024 * (kA + kB);        // a ring place
+  static constexpr int kRing = RING_;
+  static constexpr int kSlot = 4 * BM * BN;              // bytes of a tile's partial sums
+  static_assert(kA % W == 0 && kB % W == 0, "every wave issues the same loads");
+  static_assert(BM % 64 == 0 && 64 * BN * 4 <= kRing * kPlace, "the epilogue's stage fits the ring");
+};
 
 struct WideArgs {
   const u32x4_t* __restrict__ dense;
@@ -147,7 +172,7 @@ struct WideArgs {
   Epilogue e;
   int M, K, Gr, Gc, mt;   // mt: tiles of outputs
   int e0, e1, S, T, i4;
-  int remap;
+  int splits;
 };
 
 // The rows of an output tile: expert, its first slot and how many, and the
@@ -166,9 +191,10 @@ __device__ __forceinline__ void run_of(const WideArgs& a, int e, int* lo, int* h
   *hi = min(max(a.slots[e + 1], *lo), a.S);
 }
 
-// Tiles of the group's experts before expert lane e, and their number: every
-// wave scans the runs, 64 experts at a time.
-template <class Fn>
+// Scans the runs of the group's experts, 64 at a time: found(first expert,
+// tiles before, this lane's tiles of rows, inclusive tiles up to this lane, its
+// run) until it returns true.  Returns the tiles seen.
+template <int BN, class Fn>
 __device__ __forceinline__ int scan_runs(const WideArgs& a, int lane, Fn found) {
   int before = 0;
   for (int b = a.e0; b < a.e1; b += 64) {
@@ -176,17 +202,18 @@ __device__ __forceinline__ int scan_runs(const WideArgs& a, int lane, Fn found) 
     int lo, hi;
     run_of(a, e, &lo, &hi);
     if (b + lane >= a.e1) hi = lo;
-    const uint32_t nt = static_cast<uint32_t>(hi - lo + kWideN - 1) / kWideN;
+    const uint32_t nt = static_cast<uint32_t>(hi - lo + BN - 1) / BN;
     const uint32_t incl = wave_inclusive_scan(nt * a.mt);
-    if (found(b, before, nt, incl, lo, hi)) return before;
+    if (found(b, before, nt, incl, lo, hi)) break;
     before += __builtin_amdgcn_readlane(incl, 63);
   }
   return before;
 }
 
+template <class C>
 __device__ __forceinline__ WideTile wide_tile(const WideArgs& a, int t, int lane) {
   WideTile r{};
-  scan_runs(a, lane, [&](int b, int before, uint32_t nt, uint32_t incl, int lo, int hi) {
+  scan_runs<C::BN>(a, lane, [&](int b, int before, uint32_t nt, uint32_t incl, int lo, int hi) {
     const uint64_t past = __ballot(before + static_cast<int>(incl) > t);
     if (!past) return false;
     const int l = __builtin_ctzll(past);
@@ -198,231 +225,347 @@ __device__ __forceinline__ WideTile wide_tile(const WideArgs& a, int t, int lane
     const int wide = min(8, ntl - 8 * blk);
     const int m = i / wide, n = 8 * blk + (i - m * wide);
     r.e = b + l;
-    r.strip0 = m * (kWideM / kGT);
-    const int row0 = __builtin_amdgcn_readlane(lo, l) + n * kWideN;
-    r.row0 = row0;
-    r.n = min(kWideN, __builtin_amdgcn_readlane(hi, l) - row0);
+    r.strip0 = m * (C::BM / kGT);
+    r.row0 = __builtin_amdgcn_readlane(lo, l) + n * C::BN;
+    r.n = min(C::BN, __builtin_amdgcn_readlane(hi, l) - r.row0);
     return true;
   });
   return r;
 }
 
-__global__ __launch_bounds__(kWideThreads, 2) void wide_kernel(WideArgs a) {
-  // A ring of four half columns (32 k) of both operands, each 16 KB of A
-  // (4 strips x 4 fragments x 1 KB) and 16 KB of B (256 rows x 64 B).
-  __shared__ __attribute__((aligned(16))) uint8_t smem[4][32768];
+// The kernel's arguments, read again from where the launch put them: what the
+// epilogue needs is then loaded there and holds no register over the product.
+typedef const __attribute__((address_space(4))) WideArgs* ArgsAgain;
+__device__ __forceinline__ ArgsAgain args_again() {
+  ArgsAgain p = (ArgsAgain)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+
+// The epilogue of a tile.  The sums pass through LDS, 64 outputs by BN rows
+// at a time, so that a row's 64 outputs are stored together; the 16-byte unit
+// u of row n lies at u ^ (n % 16), which keeps writes and reads off each
+// other's banks.  A thread stores the same four outputs of several rows, whose
+// operands it loads while the sums arrive.  Rows and outputs past the tile's
+// are cut by the bounds of the buffer accesses.
+template <class C>
+__device__ __forceinline__ void wide_finish(uint8_t* smem, const f32x4_t (&acc)[C::MF][C::NF], const WideTile& t,
+                                            int wm, int wn, int me) {
+  constexpr int MF = C::MF, NF = C::NF;
+  constexpr int kStep = C::kThreads / 16, kRows = C::BN / kStep, kBatch = kRows < 8 ? kRows : 8;
+  const ArgsAgain z = args_again();
+  f32x4_t* stage = reinterpret_cast<f32x4_t*>(smem);
+  auto unit = [](int n, int u) { return 16 * n + (u ^ (n & 15)); };
+  const int m0 = t.strip0 * kGT, m_end = min(C::BM, z->M - m0);
+  // A [rows][ld] operand of the tile from its first element on.
+  auto tile_rsrc = [&](const void* p, int64_t ld, int size) {
+    const uint8_t* at = static_cast<const uint8_t*>(p) + (t.row0 * ld + m0) * size;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(at), 0,
+                                             static_cast<int>(((t.n - 1) * ld + m_end) * size), kBufferRsrcWord3);
+  };
+  const bool f16out = z->e.f16out, has_mul = z->e.mul != nullptr, has_res = z->e.res != nullptr;
+  const int size = f16out ? 2 : 4, ld_mul = static_cast<int>(z->e.ld_mul), ld_res = static_cast<int>(z->e.ld_res);
+  const auto ry = tile_rsrc(z->Y, z->M, size);
+  const auto rmul = tile_rsrc(z->e.mul, ld_mul, 2), rres = tile_rsrc(z->e.res, ld_res, 2);
+  const int act = z->e.act;
+#pragma unroll 1
+  for (int p = 0; p < C::BM / 64; ++p) {
+    asm volatile("" : "+v"(me));
+    const int u = me & 15, n0 = me >> 4;
+    const int m = 64 * p + 4 * u;
+    const bool mine = m < m_end;
+    f32x4_t bias = {0.f, 0.f, 0.f, 0.f}, scale = {1.f, 1.f, 1.f, 1.f};
+    const int64_t em = static_cast<int64_t>(z->M) * t.e + m0 + m;
+    if (mine && z->e.bias) bias = load_half4(z->e.bias + em);
+    if (mine && z->i4) scale = load_half4(z->scales + em);
+    // Byte offset of row n0 + kStep j, past every bound for outputs that are not ours.
+    auto at = [&](int j, int ld, int bytes) { return mine ? ((n0 + kStep * j) * ld + m) * bytes : 0x7FFFFFF0; };
+    half4_t mul[kBatch], res[kBatch];
+    auto operands = [&](int j0) {
+      if (has_mul) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          mul[j] = __builtin_bit_cast(half4_t, __builtin_amdgcn_raw_buffer_load_b64(rmul, at(j0 + j, ld_mul, 2), 0, 0));
+      }
+      if (has_res) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          res[j] = __builtin_bit_cast(half4_t, __builtin_amdgcn_raw_buffer_load_b64(rres, at(j0 + j, ld_res, 2), 0, 0));
+      }
+    };
+    operands(0);
+    const int row = me & 15, kb = (me >> 4) & 3;
+#pragma unroll
+    for (int f = 0; f < MF; ++f)
+      if ((MF * wm + f) / 4 == p) {
+#pragma unroll
+        for (int nb = 0; nb < NF; ++nb)
+          stage[unit(16 * (NF * wn + nb) + row, (4 * (MF * wm + f) + kb) & 15)] = acc[f][nb];
+      }
+    __syncthreads();
+    auto emit = [&](auto kind) {
+#pragma unroll 1
+      for (int j0 = 0; j0 < kRows; j0 += kBatch) {
+        asm volatile("" : "+v"(me));
+        if (j0 > 0) operands(j0);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          f32x4_t v = stage[unit((me >> 4) + kStep * (j0 + j), me & 15)] * scale + bias;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = activation<decltype(kind)::value>(v[i]);
+          if (has_mul) v *= to_float4(mul[j]);
+          if (has_res) v += to_float4(res[j]);
+          if (f16out)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2_t, to_half4(v)), ry,
+                                                  at(j0 + j, z->M, 2), 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), ry, at(j0 + j, z->M, 4), 0, 0);
+        }
+      }
+    };
+    switch (act) {
+      case USW_ACT_RELU: emit(std::integral_constant<int, USW_ACT_RELU>{}); break;
+      case USW_ACT_GELU: emit(std::integral_constant<int, USW_ACT_GELU>{}); break;
+      case USW_ACT_GELU_TANH: emit(std::integral_constant<int, USW_ACT_GELU_TANH>{}); break;
+      case USW_ACT_SILU: emit(std::integral_constant<int, USW_ACT_SILU>{}); break;
+      default: emit(std::integral_constant<int, USW_ACT_NONE>{});
+    }
+    __syncthreads();
+  }
+}
+
+template <class C>
+__global__ __launch_bounds__(C::kThreads, 2) void wide_kernel(WideArgs a) {
+  constexpr int MF = C::MF, NF = C::NF, W = C::W;
+  // The ring: places of a half column (32 k) of both operands, kA KB of
+  // weight fragments, then kB blocks of 16 rows of x, 64 bytes a row.
+  __shared__ __attribute__((aligned(16))) uint8_t smem[C::kRing * C::kPlace];
   __shared__ uint32_t last_flag;
   USW_LDS_POISON(smem);
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = w & 1, wn = w >> 1;
+  const int wm = w % C::WM, wn = w / C::WM;
   const int row = lane & 15, kb = lane >> 4;
-  const int P = static_cast<int>(gridDim.x);
+
+  // Workgroups are dealt to the 8 XCDs in turn; XCD i takes the i-th eighth
+  // of the pieces or, streaming, is workgroups i P / 8 on, so that neighbours
+  // share their operands in its L2.
+  const int tiles = a.slots
+                        ? scan_runs<C::BN>(a, lane, [](int, int, uint32_t, uint32_t, int, int) { return false; })
+                        : (a.S + C::BN - 1) / C::BN * a.mt;
   const int b = static_cast<int>(blockIdx.x);
-  const int L = a.remap ? (b & 7) * (P >> 3) + (b >> 3) : b;
+  int L;
+  // Streaming: R rounds of whole tiles; the U units (tile, column) from B on,
+  // of the tiles left over, are shared evenly by Pr workgroups, this one's
+  // being [r0, u1).
+  int P = 0, R = 0, Pr = 0;
+  int64_t B = 0, U = 0, r0 = 0, u1 = 0;
   const int64_t Gc = a.Gc;
-
-  const int tiles = a.slots ? scan_runs(a, lane, [](int, int, uint32_t, uint32_t, int, int) { return false; })
-                            : (a.S + kWideN - 1) / kWideN * a.mt;
-  const int R = tiles / P;
-  const int64_t B = static_cast<int64_t>(R) * P * Gc;          // units (tile, column) of the whole rounds
-  const int64_t U = static_cast<int64_t>(tiles - R * P) * Gc;  // units of the tiles left over
-  const int64_t Pr = min(static_cast<int64_t>(P), max(int64_t(1), U / kWideMinCols));   // workgroups that share them
-  int64_t r0 = 0, r1 = 0;
-  if (L < Pr) {
-    r0 = B + U * L / Pr;
-    r1 = B + U * (L + 1) / Pr;
+  if constexpr (C::kStream) {
+    P = static_cast<int>(gridDim.x);
+    L = (b & 7) * (P >> 3) + (b >> 3);   // P is a multiple of 8
+    R = tiles / P;
+    B = static_cast<int64_t>(R) * P * Gc;
+    U = static_cast<int64_t>(tiles - R * P) * Gc;
+    Pr = min(P, max(tiles - R * P, static_cast<int>(U / kStreamMinCols)));
+    if (L < Pr) {
+      r0 = B + U * L / Pr;
+      u1 = B + U * (L + 1) / Pr;
+    }
+  } else {
+    const int pieces = tiles * a.splits;
+    const int per = (pieces + 7) / 8;
+    L = (b & 7) * per + (b >> 3);
+    if ((b >> 3) >= per || L >= pieces) return;
   }
-
-  // Stores four sums: row n of the tile, outputs m .. m+3.
-  auto store4 = [&](const WideTile& t, int n, int m, f32x4_t v) {
-    if (n >= t.n || m >= a.M) return;
-    if (a.i4) v *= load_half4(a.scales + static_cast<int64_t>(a.M) * t.e + m);
-    Epilogue e = a.e;
-    if (e.bias) e.bias += static_cast<int64_t>(a.M) * t.e;
-    epilogue_store4(e, a.Y, a.M, static_cast<int64_t>(t.row0) + n, m, v);
-  };
-
-  // The pieces of the shared range from the last to the first, so that the
-  // workgroups of a tile start at both its ends and its sums are added while
-  // whole tiles still run; then the whole tiles.
-  int64_t u1 = r1;
-  for (int r = 0; u1 > r0 || r < R;) {
-    int tile, c_begin = 0, c_end = a.Gc;
+  // The shared pieces from the last to the first, so that the workgroups of a
+  // tile start at both its ends and its sums are added while whole tiles still
+  // run; then the whole tiles.
+  for (int round = 0; !C::kStream || u1 > r0 || round < R;) {
+  int tile, c_begin = 0, c_end = a.Gc, slot = L;
+  bool shared;
+  if constexpr (C::kStream) {
     if (u1 > r0) {
       tile = static_cast<int>((u1 - 1) / Gc);
       c_end = static_cast<int>(u1 - tile * Gc);
       c_begin = static_cast<int>(max(r0, tile * Gc) - tile * Gc);
       u1 = tile * Gc + c_begin;
+      slot = 2 * L + (u1 == r0 ? 0 : 1);
     } else {
-      tile = L + r * P;
-      ++r;
+      tile = L + round * P;
+      ++round;
     }
-    const WideTile t = wide_tile(a, tile, lane);
-    const int64_t t0 = tile * Gc;
-    const bool full = c_begin == 0 && c_end == a.Gc;
+    shared = c_begin > 0 || c_end < a.Gc;
+  } else {
+    tile = L / a.splits;
+    const int sidx = L - tile * a.splits;
+    c_begin = static_cast<int>(Gc * sidx / a.splits);
+    c_end = static_cast<int>(Gc * (sidx + 1) / a.splits);
+    shared = a.splits > 1;
+  }
+  const WideTile t = wide_tile<C>(a, tile, lane);
 
-    // This wave's share of a half column: two fragments and two blocks of 16
-    // rows of x, 1 KB a load.  Lane 4 j + i of a block's load brings piece
-    // (i - j / 4) mod 4 of row j, so piece q of row r lies at (q + r / 4) mod 4
-    // and the 16 rows of a fragment spread over all banks.
-    const int strip = min(t.strip0 + (w >> 1), a.Gr - 1);
-    const u32x4_t* wsrc = a.dense + ((static_cast<int64_t>(t.e - a.e0) * a.Gr + strip) * Gc + c_begin) * 512 + 128 * (w & 1) + lane;
-    const uint16_t* xsrc[2];
+  // This wave's loads of a half column: fragments w, w + W, ... of the weight
+  // and blocks w, w + W, ... of x.  Lane 4 j + i of a block's load brings
+  // piece (i - j / 4) mod 4 of row j, so piece q of row r lies at
+  // (q + r / 4) mod 4 and the 16 rows of a fragment spread over all banks.
+  const u32x4_t* wsrc[C::kA / W];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int s = t.row0 + min(16 * (2 * w + j) + (lane >> 2), t.n - 1);
-      const uint32_t xr = min(static_cast<uint32_t>(a.rows ? a.rows[s] : s), static_cast<uint32_t>(a.T - 1));
-      xsrc[j] = a.X + static_cast<int64_t>(xr) * a.K + c_begin * kGT + 8 * ((lane - (lane >> 4)) & 3);
+  for (int j = 0; j < C::kA / W; ++j) {
+    const int i = w + W * j;
+    const int strip = min(t.strip0 + (i >> 2), a.Gr - 1);
+    wsrc[j] = a.dense + ((static_cast<int64_t>(t.e - a.e0) * a.Gr + strip) * a.Gc + c_begin) * 512 + 64 * (i & 3) + lane;
+  }
+  const uint16_t* xsrc[C::kB / W];
+#pragma unroll
+  for (int j = 0; j < C::kB / W; ++j) {
+    const int s = t.row0 + min(16 * (w + W * j) + (lane >> 2), t.n - 1);
+    const uint32_t xr = min(static_cast<uint32_t>(a.rows ? a.rows[s] : s), static_cast<uint32_t>(a.T - 1));
+    xsrc[j] = a.X + static_cast<int64_t>(xr) * a.K + c_begin * kGT + 8 * ((lane - (lane >> 4)) & 3);
+  }
+  const uint32_t ldst = lds_addr(smem) + 1024 * w;
+  const int H = 2 * (c_end - c_begin);   // half columns of the piece
+  auto load = [&](int h, uint32_t place) {
+#pragma unroll
+    for (int j = 0; j < C::kA / W; ++j) lds_dma16(wsrc[j] + static_cast<int64_t>(h) * 256, ldst + place + 1024 * W * j);
+#pragma unroll
+    for (int j = 0; j < C::kB / W; ++j) lds_dma16(xsrc[j] + 32 * h, ldst + place + 1024 * (C::kA + W * j));
+  };
+
+  struct Frags {
+    half8_t a[MF], b[NF];
+  };
+  const uint8_t* abase = smem + 1024 * MF * wm + 16 * lane;
+  const uint8_t* bbase = smem + 1024 * (C::kA + NF * wn) + 64 * row + 16 * ((kb + (row >> 2)) & 3);
+  auto read = [&](Frags& f, uint32_t place) {
+#pragma unroll
+    for (int nb = 0; nb < NF; ++nb) f.b[nb] = *reinterpret_cast<const half8_t*>(bbase + place + 1024 * nb);
+#pragma unroll
+    for (int i = 0; i < MF; ++i) f.a[i] = *reinterpret_cast<const half8_t*>(abase + place + 1024 * i);
+  };
+  f32x4_t acc[MF][NF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  // Half column h: its fragments are in registers; those of h + 1 are read
+  // between its MFMAs, and the loads of h + kRing go into its own ring place,
+  // whose reads ended before the last barrier.  At the barrier half h + 2 has
+  // landed, with the loads of the kRing - 2 after it still in flight.
+  uint32_t place = 0;   // of half column h
+  auto half_column = [&](int h, const Frags& cur, Frags& nxt) {
+    const bool more = h + C::kRing < H;
+    if (more) load(h + C::kRing, place);
+    place = place == (C::kRing - 1) * C::kPlace ? 0u : place + C::kPlace;
+    read(nxt, place);
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int nb = 0; nb < NF; ++nb)
+        acc[i][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(cur.a[i], cur.b[nb], acc[i][nb], 0, 0, 0);
+    constexpr int kEach = MF * NF / (MF + NF);
+#pragma unroll
+    for (int i = 0; i < MF + NF; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);       // one LDS read
+      __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);   // MFMAs
     }
-    const uint32_t ldst = lds_addr(smem[0]) + 2048 * w;
-    const int H = 2 * (c_end - c_begin);   // half columns of the piece
-    auto load = [&](int h) {
-      const uint32_t dst = ldst + 32768 * (h & 3);
-      const u32x4_t* ws = wsrc + static_cast<int64_t>(h) * 256;
-      lds_dma16(ws, dst);
-      lds_dma16(ws + 64, dst + 1024);
-      lds_dma16(xsrc[0] + 32 * h, dst + 16384);
-      lds_dma16(xsrc[1] + 32 * h, dst + 16384 + 1024);
-    };
-
-    struct Frags {
-      half8_t a[8], b[4];
-    };
-    const uint8_t* abase = smem[0] + 8192 * wm + 16 * lane;
-    const uint8_t* bbase = smem[0] + 16384 + 64 * (64 * wn + row) + 16 * ((kb + (row >> 2)) & 3);
-    auto read = [&](Frags& f, int h) {
-      const int at = 32768 * (h & 3);
-#pragma unroll
-      for (int nb = 0; nb < 4; ++nb) f.b[nb] = *reinterpret_cast<const half8_t*>(bbase + at + 1024 * nb);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f.a[i] = *reinterpret_cast<const half8_t*>(abase + at + 1024 * i);
-    };
-    f32x4_t acc[8][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    // Half column h: its fragments are in registers; those of h + 1 are read
-    // between its MFMAs, and the loads of h + 4 go into the ring place that
-    // the reads of h left before the last barrier.  At the barrier half
-    // h + 2 has landed, with the loads of h + 3 and h + 4 still in flight.
-    auto half_column = [&](int h, const Frags& cur, Frags& nxt) {
-      const bool more = h + 4 < H;
-      if (more) load(h + 4);
-      read(nxt, h + 1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-          acc[i][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(cur.a[i], cur.b[nb], acc[i][nb], 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 12; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // two MFMAs
-      }
-      __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
-      if (more) USW_PRODUCER_BARRIER(8);
-      else USW_PRODUCER_BARRIER(0);
-    };
-    for (int h = 0; h < min(4, H); ++h) load(h);
-    if (H >= 4) USW_PRODUCER_BARRIER(8);
+    __builtin_amdgcn_sched_group_barrier(0x008, MF * NF - kEach * (MF + NF), 0);
+    if (more) ring_barrier<(C::kRing - 2) * C::kLoads>();
     else USW_PRODUCER_BARRIER(0);
-    Frags f0, f1;
-    read(f0, 0);
-    for (int h = 0; h < H; h += 2) {
-      half_column(h, f0, f1);
-      half_column(h + 1, f1, f0);
-    }
+  };
+#pragma unroll
+  for (int h = 0; h < C::kRing; ++h)
+    if (h < H) load(h, h * C::kPlace);
+  if (H >= C::kRing) ring_barrier<(C::kRing - 2) * C::kLoads>();
+  else USW_PRODUCER_BARRIER(0);
+  Frags f0, f1;
+  read(f0, 0);
+  lds_barrier();   // every wave has read place 0, which half column 0 loads into
+  for (int h = 0; h < H; h += 2) {
+    half_column(h, f0, f1);
+    half_column(h + 1, f1, f0);
+  }
 
-    // Lane l of block (f, nb): outputs 16 f + 4 (l / 16) + i, row 16 nb + l % 16 of the wave's 128 x 64.
-    // The thread's number goes through an empty asm: the addresses derived
-    // from it are computed here, not kept in registers over the product.
-    int me = tid;
-    asm volatile("" : "+v"(me));
-    const int64_t x0 = t0 - B;
-    int q0 = 0, np = 0;
-    if (!full) {
-      // A shared tile: the accumulators go to a slot in register order with
-      // stores that reach the level all XCDs share; the piece that completes
-      // the tile's count adds the slots in column order.  Owners of the tile:
-      // workgroups p with B + U p / Pr <= t0 + Gc - 1 and B + U (p + 1) / Pr > t0.
-      const int slot = 2 * L + (t0 + c_begin == r0 ? 0 : 1);
-      const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(a.part + static_cast<int64_t>(slot) * kWideSlot, 0,
-                                                          kWideSlot * 4, kBufferRsrcWord3);
-#pragma unroll
-      for (int f = 0; f < 8; ++f)
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[f][nb]), rsrc,
-                                                 (((w * 8 + f) * 4 + nb) * 64 + (me & 63)) * 16, 0, kCacheSc1);
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-      __builtin_amdgcn_s_waitcnt(0);
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-      __syncthreads();
-      q0 = static_cast<int>(((x0 + 1) * Pr + U - 1) / U) - 1;
-      np = static_cast<int>(((x0 + Gc) * Pr + U - 1) / U) - q0;
-      if (tid == 0)
-        last_flag = __hip_atomic_fetch_add(&a.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-                    static_cast<uint32_t>(np - 1);
-      __syncthreads();
-      const bool last = last_flag != 0;
-      __syncthreads();   // last_flag is read; the next piece may write it
-      if (!last) continue;
-      if (tid == 0) __hip_atomic_store(&a.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // Lane l of block (f, nb): outputs 16 f + 4 (l / 16) + i, row 16 nb + l % 16
+  // of the wave's tile.  The thread's number goes through an empty asm, here
+  // and below: what is derived from it is computed where it is used and holds
+  // no register over the product.
+  int me = tid;
+  asm volatile("" : "+v"(me));
+  bool finish = true;
+  if (shared) {
+    // The pieces of a tile leave their accumulators in slots, in register
+    // order, with stores that reach the level all XCDs share; the last to
+    // finish adds them, every lane its own, in column order.  Streaming, the
+    // owners of a tile are the workgroups p with B + U p / Pr <= t0 + Gc - 1
+    // and B + U (p + 1) / Pr > t0, t0 its first unit, and a workgroup has a
+    // slot for the piece that opens its range and one for that which closes it.
+    const int64_t t0 = tile * Gc;
+    int q0 = tile * a.splits, np = a.splits;
+    if constexpr (C::kStream) {
+      q0 = static_cast<int>(((t0 - B + 1) * Pr + U - 1) / U) - 1;
+      np = static_cast<int>(((t0 - B + Gc) * Pr + U - 1) / U) - q0;
     }
-    // Through LDS, 128 outputs by 256 rows at a time, so that a row's 128
-    // outputs are stored together; the 16-byte unit u of row n lies at
-    // u ^ (n % 32), which keeps writes and reads off each other's banks.
-    f32x4_t* tile4 = reinterpret_cast<f32x4_t*>(smem);
-    auto unit = [](int n, int u) { return 32 * n + (u ^ (n & 31)); };
-    for (int h = 0; h < 2; ++h) {
-      if (full) {
-        if (wm == h) {
+    auto slot_rsrc = [&](int64_t i) {
+      return __builtin_amdgcn_make_buffer_rsrc(a.part + i * (C::kSlot / 4), 0, C::kSlot, kBufferRsrcWord3);
+    };
+    auto slot_of = [&](int k) -> int64_t {
+      const int64_t q = q0 + k;
+      if constexpr (C::kStream) return 2 * q + (B + U * q / Pr >= t0 ? 0 : 1);
+      else return q;
+    };
+    const int at = (w * MF * NF * 64 + (me & 63)) * 16;
+    const auto own = slot_rsrc(slot);
 #pragma unroll
-          for (int f = 0; f < 8; ++f)
+    for (int i = 0; i < MF * NF; ++i)
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, acc[i / NF][i % NF]), own, at + 1024 * i, 0,
+                                             kCacheSc1);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0);
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __syncthreads();
+    if (tid == 0)
+      last_flag = __hip_atomic_fetch_add(&a.counters[tile], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                  static_cast<uint32_t>(np - 1);
+    __syncthreads();
+    finish = last_flag != 0;
+    __syncthreads();   // last_flag is read; the next piece may write it
+    if (finish) {
+      if (tid == 0) __hip_atomic_store(&a.counters[tile], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      const auto first = slot_rsrc(slot_of(0));
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb)
-              tile4[unit(64 * wn + 16 * nb + (me & 15), 4 * f + ((me >> 4) & 3))] = acc[f][nb];
-        }
-      } else {
-        // Eight elements per thread and round; element el is lane el % 64 of
-        // block (f, nb) of wave wv, el = ((wv * 8 + f) * 4 + nb) * 64 + lane;
-        // the half's waves are wv = h, h + 2, ...
-        for (int v0 = 0; v0 < 4; v0 += 2) {
-          f32x4_t sum[8], u[8];
+      for (int i = 0; i < MF * NF; ++i)
+        acc[i / NF][i % NF] =
+            __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(first, at + 1024 * i, 0, kCacheSc1));
+      constexpr int kBatch = MF * NF < 16 ? MF * NF : 16;
+      for (int k = 1; k < np; ++k) {
+        const auto r = slot_rsrc(slot_of(k));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sum[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-          for (int k = 0; k < np; ++k) {
-            const int64_t q = q0 + k;
-            const int64_t s = 2 * q + (B + U * q / Pr >= t0 ? 0 : 1);
-            const auto r = __builtin_amdgcn_make_buffer_rsrc(a.part + s * kWideSlot, 0, kWideSlot * 4, kBufferRsrcWord3);
+        for (int i0 = 0; i0 < MF * NF; i0 += kBatch) {
+          f32x4_t v[kBatch];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int el = (2 * (v0 + (j >> 2)) + h) * 2048 + 512 * (j & 3) + me;
-              u[j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, el * 16, 0, kCacheSc1));
-            }
+          for (int i = 0; i < kBatch; ++i)
+            v[i] = __builtin_bit_cast(f32x4_t,
+                                      __builtin_amdgcn_raw_buffer_load_b128(r, at + 1024 * (i0 + i), 0, kCacheSc1));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[j] += u[j];
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int in = 512 * (j & 3) + me;   // element of wave 2 (v0 + j / 4) + h
-            const int ln = in & 63, nb = (in >> 6) & 3, f = in >> 8;
-            tile4[unit(64 * (v0 + (j >> 2)) + 16 * nb + (ln & 15), 4 * f + (ln >> 4))] = sum[j];
-          }
+          for (int i = 0; i < kBatch; ++i) acc[(i0 + i) / NF][(i0 + i) % NF] += v[i];
         }
       }
-      __syncthreads();
-      for (int i = me; i < 32 * kWideN; i += kWideThreads) {
-        const int n = i >> 5, u = i & 31;
-        store4(t, n, t.strip0 * kGT + 128 * h + 4 * u, tile4[unit(n, u)]);
-      }
-      __syncthreads();
     }
   }
+  if (finish) wide_finish<C>(smem, acc, t, wm, wn, me);
+  if constexpr (!C::kStream) return;
+  }
 }
+
+using Large = Tiling<8, 4, 2, 4, 4, true>;     // 256 x 256, eight waves, one workgroup per compute unit
+using Medium = Tiling<4, 4, 2, 2, 3, false>;   // 128 x 128
+using Small = Tiling<2, 2, 2, 2, 3, false>;    // 64 x 64
+
+constexpr int kBM[3] = {Large::BM, Medium::BM, Small::BM};
+constexpr int kBN[3] = {Large::BN, Medium::BN, Small::BN};
+constexpr int64_t kComputeUnits = 256;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -438,13 +581,34 @@ WidePlan wide_plan(const Geometry& g, int32_t E, int32_t S) {
   WidePlan p{};
   const int64_t one = g.M * g.K * 2;
   p.group = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(E, kDenseBytes / one)));
-  const int64_t mt = (g.M + kWideM - 1) / kWideM;
-  const int64_t active = std::min<int64_t>(p.group, S);
-  p.tiles = (active + (S - active) / kWideN) * mt;
-  p.wgs = static_cast<int>(kComputeUnits);
-  p.cb = align256(static_cast<size_t>(4) * p.tiles);
-  p.slots_at = p.cb;
-  p.dense_at = p.slots_at + static_cast<size_t>(2) * p.wgs * kWideSlot * sizeof(float);
+  // Expected tiles of a tiling: runs end inside a tile, half a tile each.
+  const int64_t runs = std::min<int64_t>(p.group, S);
+  auto expected = [&](int t) {
+    const int64_t n = p.group == 1 ? (S + kBN[t] - 1) / kBN[t] : std::max<int64_t>(runs, S / kBN[t] + runs / 2);
+    return n * ((g.M + kBM[t] - 1) / kBM[t]);
+  };
+  // Large tiles from one whole round on; they are the fastest on the matrix
+  // cores (MI355X, fp16, expansion included: 4096^3 131 us against 174 with
+  // medium tiles, 11008x4096 N = 2048 221 / 243), but with fewer tiles too
+  // many columns are shared (11008x4096 N = 512: 99 / 88, 5120x2560 N = 1400:
+  // 77 / 58).  Small tiles up to 4e9 multiply-adds, where the grid is short of
+  // workgroups (1152x1152 N = 300: 13.2 us against 17.1 with medium tiles,
+  // 4096x4096 N = 100 26.2 / 30.4; 5120x5120 N = 200 40.5 / 40.9, N = 300
+  // 50.1 / 44.3).
+  p.tiling = expected(0) >= kComputeUnits ? 0 : g.M * g.K * S <= 4000000000ll ? 2 : 1;
+  // Splits of the columns, at least eight each, while they fill the chip: up
+  // to 256 medium workgroups (4096x11008 N = 512: 2 splits 81.4 us, 1 113.7, 4
+  // 87.7) or 704 small ones (2560x2560 N = 160: 4 splits 21.3, 1 27.3;
+  // 2048x2048 N = 70: 4 splits 15.8, 1 19.9).
+  p.splits = 1;
+  const int64_t most = p.tiling == 0 ? 0 : p.tiling == 1 ? 256 : 704;
+  while (p.splits < 8 && expected(p.tiling) * p.splits * 2 <= most && g.Gc >= 16 * p.splits) p.splits *= 2;
+  const int64_t mt = (g.M + kBM[p.tiling] - 1) / kBM[p.tiling];
+  p.tiles = (runs + (S - runs) / kBN[p.tiling]) * mt;
+  const size_t slot = static_cast<size_t>(4) * kBM[p.tiling] * kBN[p.tiling];
+  const size_t slots = p.tiling == 0 ? 2 * kComputeUnits : p.splits > 1 ? p.tiles * p.splits : 0;
+  p.cb = slots > 0 ? align256(static_cast<size_t>(4) * p.tiles) : 0;
+  p.dense_at = p.cb + slots * slot;
   p.need = p.dense_at + static_cast<size_t>(p.group) * one;
   return p;
 }
@@ -469,19 +633,22 @@ usw_status wide_launch(const WideCall& c, const Geometry& g, const WidePlan& p, 
   a.scales = c.scales;
   a.slots = c.slots;
   a.rows = c.rows;
-  a.part = reinterpret_cast<float*>(w + p.slots_at);
+  a.part = reinterpret_cast<float*>(w + p.cb);
   a.counters = reinterpret_cast<uint32_t*>(w);
   a.e = c.e;
   a.M = static_cast<int>(g.M);
   a.K = static_cast<int>(g.K);
   a.Gr = static_cast<int>(g.Gr);
   a.Gc = static_cast<int>(g.Gc);
-  a.mt = static_cast<int>((g.M + kWideM - 1) / kWideM);
+  a.mt = static_cast<int>((g.M + kBM[p.tiling] - 1) / kBM[p.tiling]);
   a.S = c.S;
   a.T = c.T;
   a.i4 = c.val_type == USW_VAL_I4;
-  a.remap = p.wgs % 8 == 0;
+  a.splits = p.splits;
   const unsigned gx = static_cast<unsigned>((g.ngt + kExpandWaves - 1) / kExpandWaves);
+  const int64_t blocks = p.tiling == 0 ? kComputeUnits : (p.tiles * p.splits + 7) / 8 * 8;
+  if (blocks >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
+  const dim3 wgrid(static_cast<unsigned>(blocks));
   for (int e0 = 0; e0 < c.E; e0 += p.group) {
     const int e1 = std::min(c.E, e0 + p.group);
     x.e0 = a.e0 = e0;
@@ -489,7 +656,9 @@ usw_status wide_launch(const WideCall& c, const Geometry& g, const WidePlan& p, 
     const dim3 grid(gx, static_cast<unsigned>(e1 - e0));
     if (a.i4) expand_kernel<true><<<grid, 64 * kExpandWaves, 0, s>>>(x);
     else expand_kernel<false><<<grid, 64 * kExpandWaves, 0, s>>>(x);
-    wide_kernel<<<p.wgs, kWideThreads, 0, s>>>(a);
+    if (p.tiling == 0) wide_kernel<Large><<<wgrid, Large::kThreads, 0, s>>>(a);
+    else if (p.tiling == 1) wide_kernel<Medium><<<wgrid, Medium::kThreads, 0, s>>>(a);
+    else wide_kernel<Small><<<wgrid, Small::kThreads, 0, s>>>(a);
     if (hipGetLastError() != hipSuccess) return USW_ERR_HIP;
   }
   return USW_OK;
