@@ -654,7 +654,10 @@ typedef struct usw_epilogue {
  * Workspace of usw_spmm_fused (0 when none) and its leading counter bytes,
  * with usw_spmm_ex's rules: the counters must be zero when a call starts and
  * are zero again when it ends, and calls that may overlap need workspaces of
- * their own.
+ * their own.  A call has no counters or at least 64 KiB of them, and uses the
+ * first 64 KiB of its workspace for nothing else, so calls of any sizes may
+ * take turns on a workspace whose first 64 KiB were zeroed once, while none
+ * reports more counter bytes than that.
  */
 usw_status usw_spmm_fused_workspace(const usw_fmt* fmt, int32_t N, int32_t splits, size_t* bytes,
                                     size_t* counter_bytes);

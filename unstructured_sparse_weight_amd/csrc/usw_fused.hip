@@ -46,8 +46,6 @@ usw_status make_epilogue(const usw_epilogue* ep, int64_t M, int32_t y_type, Epil
   return USW_OK;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 // ---------------------------------------------------------------------------
 // One weight
 // ---------------------------------------------------------------------------
@@ -88,7 +86,10 @@ FusedPlan plan_fused(const usw_fmt* f, const usw::Geometry& g, int32_t N, int sp
   }
   c.p = make_plan<FusedArgs>(g, N, splits_req, f->val_type == USW_VAL_I4, lean_values(f, g));
   c.need = workspace_bytes(g, c.p);
-  c.cb = c.need > 0 ? counters_bytes(g) : 0;
+  if (c.need > 0) {
+    c.cb = usw::counter_zone(counters_bytes(g));
+    c.need += c.cb - counters_bytes(g);
+  }
   return c;
 }
 
@@ -219,7 +220,7 @@ ExpertPlan plan_expert(const usw_expert_fmt* f, const usw::Geometry& g, int32_t 
   const Plan one = make_plan<ExpertArgs>(gt, chunk, 0, i4, p.lean);
   p.splits = one.splits;
   if (p.splits > 1) {
-    p.cb = align256(static_cast<size_t>(4) * p.tiles * g.Gr);
+    p.cb = usw::counter_zone(static_cast<size_t>(4) * p.tiles * g.Gr);
     p.need = p.cb + static_cast<size_t>(p.splits) * S * g.M * sizeof(float);
   }
   return p;

@@ -11,6 +11,14 @@
 
 namespace usw {
 
+// Leading workspace bytes that hold `bytes` of counters.  At least 64 KiB, which
+// no call uses for anything else, so that calls of different sizes can share a
+// workspace whose counters stay zero.
+inline size_t counter_zone(size_t bytes) {
+  constexpr size_t kLeast = size_t(64) << 10;
+  return bytes <= kLeast ? kLeast : (bytes + 255) & ~size_t(255);
+}
+
 // One call: a single weight (slots null, one run of S rows) or E weights on
 // the runs slots[E+1].  The encodings are as in usw_expert_fmt.
 struct WideCall {
@@ -34,7 +42,7 @@ struct WidePlan {
   int tiling;       // 0, 1, 2: large, medium, small tiles
   int splits;       // workgroups that share a tile's columns
   int64_t tiles;    // most output tiles of one group
-  size_t cb, dense_at, need;   // workspace: counters, partial sums, then the dense fragments
+  size_t cb, slots_at, dense_at, need;   // workspace: counters (0: none), partial sums, dense fragments
 };
 
 WidePlan wide_plan(const Geometry& g, int32_t E, int32_t S);

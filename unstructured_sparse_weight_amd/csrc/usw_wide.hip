@@ -567,8 +567,6 @@ constexpr int kBM[3] = {Large::BM, Medium::BM, Small::BM};
 constexpr int kBN[3] = {Large::BN, Medium::BN, Small::BN};
 constexpr int64_t kComputeUnits = 256;
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 // Dense fragments held at a time: weights beyond this are expanded and
 // multiplied in groups, each with its own pair of launches.
 constexpr int64_t kDenseBytes = int64_t(1) << 30;
@@ -607,8 +605,9 @@ WidePlan wide_plan(const Geometry& g, int32_t E, int32_t S) {
   p.tiles = (runs + (S - runs) / kBN[p.tiling]) * mt;
   const size_t slot = static_cast<size_t>(4) * kBM[p.tiling] * kBN[p.tiling];
   const size_t slots = p.tiling == 0 ? 2 * kComputeUnits : p.splits > 1 ? p.tiles * p.splits : 0;
-  p.cb = slots > 0 ? align256(static_cast<size_t>(4) * p.tiles) : 0;
-  p.dense_at = p.cb + slots * slot;
+  p.slots_at = counter_zone(slots > 0 ? static_cast<size_t>(4) * p.tiles : 0);
+  p.cb = slots > 0 ? p.slots_at : 0;
+  p.dense_at = p.slots_at + slots * slot;
   p.need = p.dense_at + static_cast<size_t>(p.group) * one;
   return p;
 }
@@ -633,7 +632,7 @@ usw_status wide_launch(const WideCall& c, const Geometry& g, const WidePlan& p, 
   a.scales = c.scales;
   a.slots = c.slots;
   a.rows = c.rows;
-  a.part = reinterpret_cast<float*>(w + p.cb);
+  a.part = reinterpret_cast<float*>(w + p.slots_at);
   a.counters = reinterpret_cast<uint32_t*>(w);
   a.e = c.e;
   a.M = static_cast<int>(g.M);

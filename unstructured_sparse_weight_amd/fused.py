@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
 
 from ._lib import (USW_ACT, USW_OUT_F16, USW_OUT_F32, USW_VAL_I4, UswEpilogue, UswExpertFmt, UswFmt,  # noqa: F401
                    check, lib)
@@ -107,47 +108,46 @@ def _out_type(dtype, what):
     return t
 
 
-class _On:
-    """The stream of a call and, for the call's duration, its device (and the
-    stream, when it is not the current one) as torch's current ones."""
+def _on(device, stream, body):
+    """body(raw stream handle) with ``device`` and the call's stream as
+    torch's current ones, where its allocations then go."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a GPU")
+    if stream is None:
+        if torch.cuda.current_device() == device.index:
+            return body(torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(device):
+            return body(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream.device_index != device.index:
+        raise ValueError("the stream is of another device than the tensors")
+    with torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError("the tensors must be on a GPU")
-        self.stream = torch.cuda.current_stream(device) if stream is None else stream
-        if self.stream.device_index != device.index:
-            raise ValueError("the stream is of another device than the tensors")
-        self.handle = self.stream.cuda_stream
-        self.guard = None
-        if stream is not None:
-            self.guard = torch.cuda.stream(stream)
-        elif torch.cuda.current_device() != device.index:
-            self.guard = torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
+_WS = {}   # (device index, raw stream) -> [workspace, its leading bytes that are zero between calls]
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            return self.guard.__exit__(*exc)
-        return False
 
-    def workspace(self, nbytes, counter_bytes):
-        """The workspace of a call that needs nbytes > 0, its counter bytes
-        zero.  Outside capture it is the binding's, one per stream; a captured
-        call gets one from the graph's pool, because a graph may be replayed
-        at the same time as other work of the stream it was captured on."""
-        import torch
-        if torch.cuda.is_current_stream_capturing():
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.stream.device)
-            if counter_bytes:
-                ws[:counter_bytes].zero_()
-            return ws
-        from . import _workspace
-        return _workspace(self.stream, nbytes, counter_bytes)
+def _workspace(device, handle, nbytes, counter_bytes):
+    """The workspace of a call that needs nbytes > 0, its counter bytes zero.
+    Outside capture it is the binding's, one per stream, which orders its uses; every
+    call leaves its counters zero again.  A captured call gets one from the
+    graph's pool, because a graph may be replayed at the same time as other
+    work of the stream it was captured on."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if counter_bytes:
+            ws[:counter_bytes].zero_()
+        return ws
+    ent = _WS.get((device.index, handle))
+    if ent is None or ent[0].numel() < nbytes:
+        ent = _WS[(device.index, handle)] = [torch.empty(nbytes, dtype=torch.uint8, device=device), 0]
+    if counter_bytes:      # none, or 64 KiB and more; calls without leave those alone
+        if ent[1] < counter_bytes:
+            ent[0][:counter_bytes].zero_()
+        ent[1] = counter_bytes
+    return ent[0]
 
 
 def _rows_operand(t, rows, M, device, what):
@@ -157,35 +157,35 @@ def _rows_operand(t, rows, M, device, what):
         raise ValueError(f"{what} must be [{rows}][{M}] float16")
     if t.device != device:
         raise ValueError(f"{what} is on another device")
-    if t.stride(1) != 1 or t.stride(0) % 8 or t.stride(0) < M or t.data_ptr() & 15:
-        t = t.contiguous()
-    return t
+    ld, one = t.stride()
+    if rows == 1:
+        ld = M
+    if one != 1 or ld & 7 or ld < M or ld > 1 << 20 or t.data_ptr() & 15:
+        t, ld = t.clone(memory_format=torch.contiguous_format), M
+    return t, ld
 
 
 def _epilogue(bias, act, mul, residual, rows, M, bias_shape, device):
     """(usw_epilogue, the tensors it points to)."""
-    import torch
     code = USW_ACT.get(act)
     if code is None:
         raise ValueError(f"act must be one of {', '.join(USW_ACT)}")
-    keep = []
-    ep = UswEpilogue(None, None, None, 0, 0, code, 0)
+    bp = mp = rp = None
+    ld_mul = ld_res = 0
     if bias is not None:
-        if bias.dtype != torch.float16 or tuple(bias.shape) != bias_shape or bias.device != device:
+        import torch
+        if bias.dtype != torch.float16 or bias.shape != bias_shape or bias.device != device:
             raise ValueError(f"bias must be {list(bias_shape)} float16 on the weight's device")
         if not bias.is_contiguous() or bias.data_ptr() & 15:
             bias = bias.clone(memory_format=torch.contiguous_format)
-        keep.append(bias)
-        ep.bias = bias.data_ptr()
+        bp = bias.data_ptr()
     if mul is not None:
-        mul = _rows_operand(mul, rows, M, device, "mul")
-        keep.append(mul)
-        ep.mul, ep.ld_mul = mul.data_ptr(), mul.stride(0) if rows > 1 else 0
+        mul, ld_mul = _rows_operand(mul, rows, M, device, "mul")
+        mp = mul.data_ptr()
     if residual is not None:
-        residual = _rows_operand(residual, rows, M, device, "residual")
-        keep.append(residual)
-        ep.res, ep.ld_res = residual.data_ptr(), residual.stride(0) if rows > 1 else 0
-    return ep, keep
+        residual, ld_res = _rows_operand(residual, rows, M, device, "residual")
+        rp = residual.data_ptr()
+    return UswEpilogue(bp, mp, rp, ld_mul, ld_res, code, 0), (bias, mul, residual)
 
 
 def _activations(x, K, device):
@@ -203,11 +203,21 @@ def _output(y, shape, out_dtype, device, what="y"):
     import torch
     if y is None:
         return torch.empty(shape, dtype=out_dtype or torch.float16, device=device)
-    if tuple(y.shape) != shape or not y.is_contiguous() or y.device != device:
+    if y.shape != shape or not y.is_contiguous() or y.device != device:
         raise ValueError(f"{what} must be a contiguous {list(shape)} tensor on the weight's device")
     if out_dtype is not None and y.dtype != out_dtype:
         raise ValueError(f"{what} is not of out_dtype")
     return y
+
+
+@lru_cache(maxsize=4096)
+def _fused_sizes(M, K, gt_m, gt_k, val_type, nnz, N, splits):
+    """(workspace bytes, counter bytes): a function of the sizes alone."""
+    f = UswFmt(M, K, gt_m, gt_k, val_type, 0, nnz, None, None, None, None)
+    need, cb = ctypes.c_size_t(), ctypes.c_size_t()
+    check(lib().usw_spmm_fused_workspace(ctypes.byref(f), N, splits, ctypes.byref(need), ctypes.byref(cb)),
+          "usw_spmm_fused")
+    return need.value, cb.value
 
 
 def spmm_fused(enc, x, bias=None, act: str = "none", mul=None, residual=None, y=None, out_dtype=None,
@@ -221,28 +231,36 @@ def spmm_fused(enc, x, bias=None, act: str = "none", mul=None, residual=None, y=
     tensor.  Encodings have 64x64 GroupTiles and fp16 or INT4 values.
     """
     dev = enc.device
-    with _On(dev, stream) as on:
-        x = _activations(x, enc.K, dev)
-        N = x.shape[0]
-        ep, keep = _epilogue(bias, act, mul, residual, N, enc.M, (enc.M,), dev)
-        y = _output(y, (N, enc.M), out_dtype, dev)
-        yt = _out_type(y.dtype, "y")
-        f = enc.fmt()
-        L = lib()
-        need, cb = ctypes.c_size_t(), ctypes.c_size_t()
-        check(L.usw_spmm_fused_workspace(ctypes.byref(f), N, splits, ctypes.byref(need), ctypes.byref(cb)),
-              "usw_spmm_fused")
-        ws = on.workspace(need.value, cb.value) if need.value else None
-        check(L.usw_spmm_fused(ctypes.byref(f), x.data_ptr(), y.data_ptr(), yt, N, ctypes.byref(ep), splits,
-                               ws.data_ptr() if ws is not None else None, need.value, on.handle), "usw_spmm_fused")
-    return y
+
+    def body(handle):
+        xc = _activations(x, enc.K, dev)
+        N, M = xc.shape[0], enc.M
+        ep, keep = _epilogue(bias, act, mul, residual, N, M, (M,), dev)
+        out = _output(y, (N, M), out_dtype, dev)
+        yt = _out_type(out.dtype, "y")
+        need, cb = _fused_sizes(M, enc.K, enc.gt_m, enc.gt_k, enc.val_type, enc.nnz, N, splits)
+        ws = _workspace(dev, handle, need, cb) if need else None
+        check(lib().usw_spmm_fused(ctypes.byref(enc.fmt()), xc.data_ptr(), out.data_ptr(), yt, N, ctypes.byref(ep),
+                                   splits, ws.data_ptr() if need else None, need, handle), "usw_spmm_fused")
+        return out
+
+    return _on(dev, stream, body)
 
 
 def _index(t, shape, device, what):
     import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != device:
+    if t.dtype != torch.int32 or t.shape != shape or t.device != device:
         raise ValueError(f"{what} must be {list(shape)} int32 on the same device")
     return t if t.is_contiguous() else t.contiguous()
+
+
+@lru_cache(maxsize=4096)
+def _expert_sizes(E, M, K, val_type, nnz, values_bytes, S):
+    f = UswExpertFmt(E, M, K, val_type, 0, nnz, values_bytes, None, None, None, None, None)
+    need, cb = ctypes.c_size_t(), ctypes.c_size_t()
+    check(lib().usw_expert_spmm_workspace(ctypes.byref(f), S, ctypes.byref(need), ctypes.byref(cb)),
+          "usw_expert_spmm")
+    return need.value, cb.value
 
 
 def expert_spmm(bank: ExpertBank, x, offsets, rows=None, bias=None, act: str = "none", mul=None, y=None,
@@ -256,29 +274,36 @@ def expert_spmm(bank: ExpertBank, x, offsets, rows=None, bias=None, act: str = "
     mul [S][M].  Rows of Y from offsets[E] on are left as they were (in a Y
     made here: whatever the memory held)."""
     dev = bank.device
-    with _On(dev, stream) as on:
-        x = _activations(x, bank.K, dev)
-        T = x.shape[0]
-        offsets = _index(offsets, (bank.E + 1,), dev, "offsets")
-        S = T
+
+    def body(handle):
+        xc = _activations(x, bank.K, dev)
+        T, M = xc.shape[0], bank.M
+        off = _index(offsets, (bank.E + 1,), dev, "offsets")
+        S, at = T, None
         if rows is not None:
             if rows.dim() != 1:
                 raise ValueError("rows must be [S] int32")
             S = rows.shape[0]
-            rows = _index(rows, (S,), dev, "rows")
-        ep, keep = _epilogue(bias, act, mul, None, S, bank.M, (bank.E, bank.M), dev)
-        y = _output(y, (S, bank.M), out_dtype, dev)
-        yt = _out_type(y.dtype, "y")
-        f = bank.fmt()
-        L = lib()
-        need, cb = ctypes.c_size_t(), ctypes.c_size_t()
-        check(L.usw_expert_spmm_workspace(ctypes.byref(f), S, ctypes.byref(need), ctypes.byref(cb)),
+            at = _index(rows, (S,), dev, "rows")
+        ep, keep = _epilogue(bias, act, mul, None, S, M, (bank.E, M), dev)
+        out = _output(y, (S, M), out_dtype, dev)
+        yt = _out_type(out.dtype, "y")
+        need, cb = _expert_sizes(bank.E, M, bank.K, bank.val_type, bank.nnz, bank.values.numel(), S)
+        ws = _workspace(dev, handle, need, cb) if need else None
+        check(lib().usw_expert_spmm(ctypes.byref(bank.fmt()), xc.data_ptr(), T, off.data_ptr(),
+                                    at.data_ptr() if at is not None else None, S, out.data_ptr(), yt,
+                                    ctypes.byref(ep), ws.data_ptr() if need else None, need, handle),
               "usw_expert_spmm")
-        ws = on.workspace(need.value, cb.value) if need.value else None
-        check(L.usw_expert_spmm(ctypes.byref(f), x.data_ptr(), T, offsets.data_ptr(),
-                                rows.data_ptr() if rows is not None else None, S, y.data_ptr(), yt, ctypes.byref(ep),
-                                ws.data_ptr() if ws is not None else None, need.value, on.handle), "usw_expert_spmm")
-    return y
+        return out
+
+    return _on(dev, stream, body)
+
+
+@lru_cache(maxsize=4096)
+def _route_size(T, E, k):
+    need = ctypes.c_size_t()
+    check(lib().usw_expert_route_workspace(T, E, k, ctypes.byref(need)), "usw_expert_route")
+    return need.value
 
 
 def expert_route(logits, k: int, renormalize: bool = True, stream=None) -> RoutePlan:
@@ -295,22 +320,24 @@ def expert_route(logits, k: int, renormalize: bool = True, stream=None) -> Route
     lt = _out_type(logits.dtype, "logits")
     dev = logits.device
     T, E = logits.shape
-    with _On(dev, stream) as on:
-        if T > 1 and (logits.stride(1) != 1 or logits.stride(0) < E) or (E > 1 and logits.stride(1) != 1):
-            logits = logits.contiguous()
-        L = lib()
-        need = ctypes.c_size_t()
-        check(L.usw_expert_route_workspace(T, E, k, ctypes.byref(need)), "usw_expert_route")
-        ints = torch.empty(3 * T * k + E + 1, dtype=torch.int32, device=dev)
-        ids, pos, rows = (ints[i * T * k:(i + 1) * T * k] for i in range(3))
-        offsets = ints[3 * T * k:]
+
+    def body(handle):
+        need = _route_size(T, E, k)
+        lg = logits
+        ld, one = lg.stride()
+        if (one != 1 and E > 1) or (ld < E and T > 1):
+            lg, ld = lg.contiguous(), E
+        n = T * k
+        # The scratch counts go behind the plan's arrays: one allocation.
+        ids, pos, rows, offsets, rest = torch.empty(3 * n + E + 1 + need // 4, dtype=torch.int32, device=dev).split(
+            (n, n, n, E + 1, need // 4))
         weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-        ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-        check(L.usw_expert_route(logits.data_ptr(), lt, logits.stride(0) if T > 1 else 0, T, E, k, int(renormalize),
-                                 ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-                                 pos.data_ptr(), ws.data_ptr() if ws is not None else None, need.value, on.handle),
-              "usw_expert_route")
-    return RoutePlan(ids.view(T, k), weights, offsets, rows, pos.view(T, k))
+        check(lib().usw_expert_route(lg.data_ptr(), lt, ld if T > 1 else 0, T, E, k, renormalize, ids.data_ptr(),
+                                     weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
+                                     rest.data_ptr() if need else None, need, handle), "usw_expert_route")
+        return RoutePlan(ids.view(T, k), weights, offsets, rows, pos.view(T, k))
+
+    return _on(dev, stream, body)
 
 
 def expert_combine(y, pos, weights, residual=None, out=None, out_dtype=None, stream=None):
@@ -325,22 +352,23 @@ def expert_combine(y, pos, weights, residual=None, out=None, out_dtype=None, str
     dev = y.device
     S, M = y.shape
     T, k = pos.shape
-    with _On(dev, stream) as on:
-        if not y.is_contiguous() or y.data_ptr() & 15:
-            y = y.clone(memory_format=torch.contiguous_format)
-        pos = _index(pos, (T, k), dev, "pos")
+
+    def body(handle):
+        yc = y if y.is_contiguous() and not y.data_ptr() & 15 else y.clone(memory_format=torch.contiguous_format)
+        p = _index(pos, (T, k), dev, "pos")
         if weights.dtype != torch.float32 or weights.shape != pos.shape or weights.device != dev:
             raise ValueError("weights must be float32 of pos's shape on the same device")
-        weights = weights.contiguous()
-        ld = 0
+        w = weights.contiguous()
+        rp, ld = None, 0
         if residual is not None:
-            residual = _rows_operand(residual, T, M, dev, "residual")
-            ld = residual.stride(0) if T > 1 else 0
-        out = _output(out, (T, M), out_dtype, dev, "out")
-        check(lib().usw_expert_combine(y.data_ptr(), yt, S, M, pos.data_ptr(), weights.data_ptr(), T, k,
-                                       residual.data_ptr() if residual is not None else None, ld, out.data_ptr(),
-                                       _out_type(out.dtype, "out"), on.handle), "usw_expert_combine")
-    return out
+            res, ld = _rows_operand(residual, T, M, dev, "residual")
+            rp = res.data_ptr()
+        o = _output(out, (T, M), out_dtype, dev, "out")
+        check(lib().usw_expert_combine(yc.data_ptr(), yt, S, M, p.data_ptr(), w.data_ptr(), T, k, rp, ld,
+                                       o.data_ptr(), _out_type(o.dtype, "out"), handle), "usw_expert_combine")
+        return o
+
+    return _on(dev, stream, body)
 
 
 def expert_ffn(x, logits, k: int, up: ExpertBank, down: ExpertBank, gate: ExpertBank = None, act: str = "silu",
