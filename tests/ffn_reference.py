@@ -23,13 +23,15 @@ def act(v, name):
     return v
 
 
-def product(Wd, x, bias=None, name="none", mul=None, res=None, out="f16", scale=None):
+def product(Wd, x, bias=None, name="none", mul=None, res=None, out="f16", codes=False):
     """(y, bound): the value in 64 bits, and the most that fp32 sums, an fp32
     epilogue and one rounding may be off it.
 
     * A sum of K exact products in fp32, in any order, is off by at most
-      (K + 1) U sum|w x|; the INT4 kernels sum codes (off from zero by 72, so
-      up to 80 in place of 8: sum|72 x| more) and scale once.
+      (K + 1) U sum|w x|; INT4 kernels sum codes and scale once, one rounding
+      more (codes times fp16 x are exact too).  With fp16 output they may be
+      off from zero by 72 (``codes``), which adds sum|72 x| times the row's
+      scale, a seventh of its largest weight.
     * Bias: one more rounding.  The activations' slopes are at most 1.13; their
       own error is that of an exponential whose argument is rounded (2 U |z|
       relative, z up to |v| (1 + 0.05 v^2) + 1) or of erf (a few U), a sum and
@@ -39,8 +41,8 @@ def product(Wd, x, bias=None, name="none", mul=None, res=None, out="f16", scale=
     Wd, x = np.asarray(Wd, dtype=np.float64), np.asarray(x, dtype=np.float64)
     v = x @ Wd.T
     mag = np.abs(x) @ np.abs(Wd).T
-    if scale is not None:
-        mag = mag + 72 * np.abs(x).sum(1)[:, None] * np.abs(np.asarray(scale, dtype=np.float64))[None, :]
+    if codes and out == "f16":
+        mag = mag + 72 / 7 * np.abs(x).sum(1)[:, None] * np.abs(Wd).max(1)[None, :]
     err = (x.shape[1] + 4) * U32 * mag
     if bias is not None:
         v = v + np.asarray(bias, dtype=np.float64)

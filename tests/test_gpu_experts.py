@@ -36,10 +36,9 @@ def half(rng, *shape, scale=1.0):
 
 
 def bank_of(E, M, K, val, seed, density=0.5, exact=False):
-    """(bank, dense weights [E][M][K] in 64 bits, scales [E][M] or None);
-    the experts' densities differ."""
+    """(bank, dense weights [E][M][K] in 64 bits); the experts' densities differ."""
     rng = np.random.default_rng(seed)
-    encs, dense, scales = [], [], []
+    encs, dense = [], []
     for e in range(E):
         mask = wl.mask_bernoulli(M, K, min(1.0, density * (0.6 + 0.8 * e / max(1, E - 1))) if E > 1 else density, rng)
         if exact:
@@ -49,11 +48,10 @@ def bank_of(E, M, K, val, seed, density=0.5, exact=False):
         encs.append(usw.encode(W, mask, dtype=val, device=DEV))
         o = ob.encode_i4(W, mask) if val == "i4" else ob.encode(W, mask)
         dense.append(ob.dense_weight(o).astype(np.float64))
-        scales.append(o.scales.astype(np.float64) if val == "i4" else None)
-    return usw.expert_bank(encs), dense, scales if val == "i4" else None
+    return usw.expert_bank(encs), dense
 
 
-def runs_reference(dense, scales, x, slots, rows, bias, name, mul, out):
+def runs_reference(dense, x, slots, rows, bias, name, mul, out, codes=False):
     """(y, bound) of the rows in runs; rows behind them are NaN."""
     S = len(rows) if rows is not None else x.shape[0]
     y = np.full((S, dense[0].shape[0]), np.nan)
@@ -64,8 +62,7 @@ def runs_reference(dense, scales, x, slots, rows, bias, name, mul, out):
             continue
         xe = x[rows[a:b]] if rows is not None else x[a:b]
         y[a:b], bound[a:b] = ref.product(Wd, xe, None if bias is None else bias[e], name,
-                                         None if mul is None else mul[a:b], None, out,
-                                         None if scales is None else scales[e])
+                                         None if mul is None else mul[a:b], None, out, codes)
     return y, bound
 
 
@@ -98,7 +95,7 @@ LOADS = {
 def test_product_by_expert(load, val, gather):
     counts = LOADS[load]
     E, M, K = len(counts), 128, 192
-    bank, dense, scales = bank_of(E, M, K, val, 10 + E)
+    bank, dense = bank_of(E, M, K, val, 10 + E)
     slots = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
     live, spare = int(slots[-1]), 5
     S = live + spare
@@ -113,7 +110,7 @@ def test_product_by_expert(load, val, gather):
         say(f"[experts] {load} {val} gather={gather} {name} {out}")
         y = torch.full((S, M), 7.0, dtype=DT[out], device=DEV)
         usw.expert_spmm(bank, gpu(x), gpu(slots), rows=gpu(rows), bias=gpu(b), act=name, mul=gpu(m), y=y)
-        want, bound = runs_reference(dense, scales, x, slots, rows, b, name, m, out)
+        want, bound = runs_reference(dense, x, slots, rows, b, name, m, out, val == "i4")
         near(y, want, bound, f"{name} {out}")
         assert torch.all(y[live:] == 7.0)            # rows behind the last run stay
 
@@ -123,7 +120,7 @@ def test_product_by_expert(load, val, gather):
 @pytest.mark.parametrize("counts", [[3, 0, 9], [40, 17, 100], [400, 3, 260]])
 def test_integer_exact_is_bitwise(val, density, counts):
     E, M, K = len(counts), 192, 320
-    bank, dense, _ = bank_of(E, M, K, val, 30, density, exact=True)
+    bank, dense = bank_of(E, M, K, val, 30, density, exact=True)
     slots = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
     S = int(slots[-1])
     rng = np.random.default_rng(31)
@@ -132,21 +129,22 @@ def test_integer_exact_is_bitwise(val, density, counts):
     mul = rng.integers(-2, 3, size=(S, M)).astype(np.float16)
     say(f"[experts] exact {val} {density} {counts}")
     y = usw.expert_spmm(bank, gpu(x), gpu(slots), bias=gpu(bias), act="relu", mul=gpu(mul), out_dtype=torch.float32)
-    want, _ = runs_reference(dense, None, x, slots, None, bias, "relu", mul, "f32")
+    want, _ = runs_reference(dense, x, slots, None, bias, "relu", mul, "f32")
     assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
 
 
 # Expanded weights: small, medium and large tiles, runs that end inside tiles,
-# and experts without rows (whose weights are not expanded).
+# and experts without rows (whose weights are not expanded).  The references
+# are of some rows of every run.
 EXPANDED = [([200, 0, 320, 131], 192, 320, "small"), ([500, 900, 0, 700], 1280, 1664, "medium"),
-            ([2100, 100, 1900, 0, 2300], 2112, 128, "small, many"), ([2100, 100, 1900, 0, 2300], 2496, 192, "large")]
+            ([2100, 100, 1900, 0, 2300], 2112, 128, "small, many"), ([2100, 300, 1900, 0, 2300], 2560, 5120, "large")]
 
 
 @pytest.mark.parametrize("counts,M,K,what", EXPANDED, ids=[e[3] for e in EXPANDED])
 @pytest.mark.parametrize("val", ["f16", "i4"])
 def test_expanded_tilings(counts, M, K, what, val):
     E = len(counts)
-    bank, dense, scales = bank_of(E, M, K, val, 100 + M)
+    bank, dense = bank_of(E, M, K, val, 100 + M)
     slots = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
     live = int(slots[-1])
     S = live + 7
@@ -161,8 +159,12 @@ def test_expanded_tilings(counts, M, K, what, val):
     assert torch.all(y[live:] == 7.0)
     z = usw.expert_spmm(bank, gpu(x), gpu(slots), rows=gpu(rows), bias=gpu(bias), act="relu")
     assert torch.equal(y[:live], z[:live])
-    want, bound = runs_reference(dense, scales, x, slots, rows, bias, "relu", None, "f16")
-    near(y, want, bound, what)
+    for e in range(E):
+        if counts[e] == 0:
+            continue
+        r = np.unique(np.concatenate([[slots[e], slots[e + 1] - 1], rng.integers(slots[e], slots[e + 1], 30)]))
+        want, bound = ref.product(dense[e], x[rows[r]], bias[e], "relu", None, None, "f16")
+        near(y[torch.from_numpy(r).to(DEV)], want, bound, f"{what}, expert {e}")
 
 
 def test_long_rows_split_k_twice_the_same():
@@ -170,14 +172,14 @@ def test_long_rows_split_k_twice_the_same():
     same bits."""
     E, M, K = 4, 128, 5120
     for val in ("f16", "i4"):
-        bank, dense, scales = bank_of(E, M, K, val, 40)
+        bank, dense = bank_of(E, M, K, val, 40)
         slots = np.array([0, 1, 1, 4, 6], dtype=np.int32)
         rng = np.random.default_rng(41)
         x = half(rng, 6, K)
         say(f"[experts] long rows {val}")
         y = usw.expert_spmm(bank, gpu(x), gpu(slots), act="gelu_tanh")
         assert torch.equal(y, usw.expert_spmm(bank, gpu(x), gpu(slots), act="gelu_tanh"))
-        want, bound = runs_reference(dense, scales, x, slots, None, None, "gelu_tanh", None, "f16")
+        want, bound = runs_reference(dense, x, slots, None, None, "gelu_tanh", None, "f16", val == "i4")
         near(y, want, bound, "long rows")
 
 
@@ -269,9 +271,9 @@ def test_expert_ffn(T, val, gated):
     path rounds them, so the bounds of the three products add: the down
     projection carries the hidden rows' error, at most sum |w| times it."""
     E, k, D, F = 6, 2, 128, 256
-    up, Wu, su = bank_of(E, F, D, val, 70)
-    gate, Wg, sg = bank_of(E, F, D, val, 71)
-    down, Wd, sd = bank_of(E, D, F, val, 72)
+    up, Wu = bank_of(E, F, D, val, 70)
+    gate, Wg = bank_of(E, F, D, val, 71)
+    down, Wd = bank_of(E, D, F, val, 72)
     rng = np.random.default_rng(73 + T)
     x, logits = half(rng, T, D), half(rng, T, E, scale=2.0)
     if T > 3:
@@ -290,16 +292,15 @@ def test_expert_ffn(T, val, gated):
         if a == b:
             continue
         xe = x[rows[a:b]]
-        sc = lambda s: None if s is None else s[e]  # noqa: E731
         if gated:
-            u, ub = ref.product(Wu[e], xe, bu[e], out="f16", scale=sc(su))
-            g, gb = ref.product(Wg[e], xe, bg[e], "silu", out="f32", scale=sc(sg))
+            u, ub = ref.product(Wu[e], xe, bu[e], out="f16", codes=val == "i4")
+            g, gb = ref.product(Wg[e], xe, bg[e], "silu", out="f16", codes=val == "i4")
             h = g * u
             hb = np.abs(g) * ub + gb * (np.abs(u) + ub)
             hb = hb + 2.0 ** -11 * (np.abs(h) + hb) + 2.0 ** -25
         else:
-            h, hb = ref.product(Wu[e], xe, bu[e], "silu", out="f16", scale=sc(su))
-        y[a:b], ybound[a:b] = ref.product(Wd[e], h, bd[e], out="f16", scale=sc(sd))
+            h, hb = ref.product(Wu[e], xe, bu[e], "silu", out="f16", codes=val == "i4")
+        y[a:b], ybound[a:b] = ref.product(Wd[e], h, bd[e], out="f16", codes=val == "i4")
         # The kernel's own sums run over its rounded hidden rows, larger by hb.
         ybound[a:b] += 1.01 * hb @ np.abs(Wd[e]).T
     want, bound = ref.combine(y, pos, weights, x, "f32")
@@ -315,9 +316,9 @@ def test_captured_and_replayed_with_other_routing():
     """One captured block: the routing, so the runs, changes between replays;
     every replay equals the eager result."""
     E, k, D, F, T = 8, 2, 128, 192, 40
-    up, _, _ = bank_of(E, F, D, "f16", 80)
-    gate, _, _ = bank_of(E, F, D, "f16", 81)
-    down, _, _ = bank_of(E, D, F, "f16", 82)
+    up, _ = bank_of(E, F, D, "f16", 80)
+    gate, _ = bank_of(E, F, D, "f16", 81)
+    down, _ = bank_of(E, D, F, "f16", 82)
     x = torch.randn(T, D, device=DEV).half()
     logits = torch.randn(T, E, device=DEV)
     say("[experts] graph")
@@ -347,8 +348,8 @@ def test_captured_and_replayed_with_other_routing():
 
 def test_streams_at_once():
     E, k, D, F = 4, 2, 128, 2560
-    up, _, _ = bank_of(E, F, D, "f16", 90)
-    down, _, _ = bank_of(E, D, F, "f16", 91)
+    up, _ = bank_of(E, F, D, "f16", 90)
+    down, _ = bank_of(E, D, F, "f16", 91)
     say("[experts] streams")
     made = [(torch.randn(T, D, device=DEV).half(), torch.randn(T, E, device=DEV)) for T in (5, 300)]
     want = [usw.expert_ffn(x, lg, k, up, down, act="gelu") for x, lg in made]
@@ -364,7 +365,7 @@ def test_streams_at_once():
 
 
 def test_empty_batch():
-    bank, _, _ = bank_of(2, 64, 64, "f16", 95)
+    bank, _ = bank_of(2, 64, 64, "f16", 95)
     x = torch.zeros(0, 64, dtype=torch.float16, device=DEV)
     slots = torch.zeros(3, dtype=torch.int32, device=DEV)
     say("[experts] empty")
@@ -377,7 +378,7 @@ def test_empty_batch():
 
 
 def test_refusals():
-    bank, _, _ = bank_of(2, 64, 128, "f16", 96)
+    bank, _ = bank_of(2, 64, 128, "f16", 96)
     x = torch.zeros(4, 128, dtype=torch.float16, device=DEV)
     slots = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
     rows = torch.zeros(4, dtype=torch.int32, device=DEV)

@@ -157,8 +157,9 @@ __device__ __forceinline__ int x_row(const A& a, int n, int row0) {
 
 // finish_strip with an epilogue: writes a strip's finished sums through the
 // epilogue to Y or, with split K, to split sidx's partial sums, which the
-// strip's last workgroup adds in split order and finishes.
-template <int NB, bool I4, class A, class SumFn>
+// strip's last workgroup adds in split order and finishes, AHEAD splits' loads
+// in flight.
+template <int NB, bool I4, int AHEAD, class A, class SumFn>
 __device__ __forceinline__ void finish_strip_fused(const A& a, int gi, int sidx, int nthreads, uint32_t& last_flag,
                                                    SumFn sum_of) {
   const int tid = threadIdx.x;
@@ -203,14 +204,14 @@ __device__ __forceinline__ void finish_strip_fused(const A& a, int gi, int sidx,
     const int ml = 4 * (e & 15);
     const int off = (n * a.M + m0 + ml) * 4;
     f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-    for (int p0 = 0; p0 < a.splits; p0 += 4) {
-      f32x4_t v[4];
+    for (int p0 = 0; p0 < a.splits; p0 += AHEAD) {
+      f32x4_t v[AHEAD];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < AHEAD; ++j)
         if (p0 + j < a.splits)
           v[j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(part_rsrc(p0 + j), off, 0, kCacheSc1));
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < AHEAD; ++j)
         if (p0 + j < a.splits) sum += v[j];
     }
     store_y4(n, ml, sum);
@@ -373,12 +374,16 @@ __device__ __forceinline__ uint32_t bitmap_prefix_reg(u32x2_t bm) {
 // whose bitmap table is at tab and whose values are in the LDS staging area
 // starting at vals.  INT4 rows carry the expansion's offset: corr collects
 // its correction (code_offset_collect, all four fragments of a GroupTile at once).
-template <int NB, bool I4, int F0 = 0, int F1 = 4>
+// EXACT takes the offset out of every slot instead, four packed subtractions a
+// row: the sums then round at the scale of the product and not of 72 sum|x|,
+// which an fp32 output shows (relative error 2e-7 against 4e-6) and an fp16
+// one, 2e-4 off anyway, does not; it costs 6 to 15% of the pass.
+template <int NB, bool I4, int F0 = 0, int F1 = 4, bool EXACT = false>
 __device__ __forceinline__ void tile_mma(const u32x4_t (&x)[2][NB], const uint8_t* vals, const uint8_t* tab,
                                          const uint32_t* lut, f32x4_t (&acc)[4][NB], f32x4_t (&corr)[NB],
                                          const LaneMap& lm) {
   static_assert(!I4 || (F0 == 0 && F1 == 4), "the INT4 correction covers whole GroupTiles");
-  if constexpr (I4) code_offset_collect<NB>(corr, x);
+  if constexpr (I4 && !EXACT) code_offset_collect<NB>(corr, x);
   u32x2_t e[F1 - F0][2];
 #pragma unroll
   for (int f = F0; f < F1; ++f)
@@ -391,7 +396,8 @@ __device__ __forceinline__ void tile_mma(const u32x4_t (&x)[2][NB], const uint8_
     for (int ks = 0; ks < 2; ++ks) {
       const uint32_t word = e[f - F0][ks].x;
       const uint32_t rb = e[f - F0][ks].y + __builtin_popcount(word & lm.pmask);
-      const half8_t a = rebuild_row<I4>(vals, lut, rb, __builtin_amdgcn_ubfe(word, lm.sh, 8));
+      half8_t a = rebuild_row<I4>(vals, lut, rb, __builtin_amdgcn_ubfe(word, lm.sh, 8));
+      if constexpr (I4 && EXACT) a -= static_cast<_Float16>(kCodeOffset);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
         acc[f][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(half8_t, x[ks][nb]), acc[f][nb], 0,
@@ -416,6 +422,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
   constexpr int kW = C::kWavesPerGroup;
   constexpr int kThreads = C::kThreadsPerGroup;
   constexpr int kD = C::kDepth;
+  constexpr bool kExact = ArgTraits<A>::kEpilogue && !OUT_F16;   // INT4 with fp32 output
   // Row selectors: fp16 16 nibble entries of two dwords, INT4 256 byte
   // entries of two dwords.
   __shared__ __attribute__((aligned(16))) uint32_t lut[I4 ? 512 : 32];
@@ -548,7 +555,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
       const int cn = min(c + 1, c_last);
       slot_load(s0, a, gi, cn, lane, off_at(cn), off_at(cn + 1), xrow);
       wave_sync();
-      tile_mma<NB, I4>(xc, smem, tab, lut, acc, corr, lm);
+      tile_mma<NB, I4, 0, 4, kExact>(xc, smem, tab, lut, acc, corr, lm);
       wave_sync();
       write_tab(s0);
     }
@@ -579,7 +586,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
       __builtin_amdgcn_s_setprio(0);
       slot_commit(cur, vb, lane);
       wave_sync();
-      tile_mma<NB, I4>(cur.x, smem, tab, lut, acc, corr, lm);
+      tile_mma<NB, I4, 0, 4, kExact>(cur.x, smem, tab, lut, acc, corr, lm);
       wave_sync();
       write_tab(after);
     };
@@ -594,7 +601,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
   }
 
   // Workgroup reduction over waves (fixed order).
-  if constexpr (I4) code_offset_finish<NB>(corr);
+  if constexpr (I4 && !kExact) code_offset_finish<NB>(corr);
   __syncthreads();
   float* red = reinterpret_cast<float*>(smem);   // [waves][4][NB][64 lanes][4]
 #pragma unroll
@@ -602,7 +609,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
       *reinterpret_cast<f32x4_t*>(red + (((w * 4 + f) * NB + nb) * 64 + lane) * 4) =
-          I4 ? acc[f][nb] + corr[nb] : acc[f][nb];
+          I4 && !kExact ? acc[f][nb] + corr[nb] : acc[f][nb];
   __syncthreads();
 
   auto sum_of = [&](int n, int ml) {
@@ -618,7 +625,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
     return sum;
   };
   if constexpr (ArgTraits<A>::kEpilogue)
-    finish_strip_fused<NB, I4>(a, gi, sidx, kThreads, last_flag, sum_of);
+    finish_strip_fused<NB, I4, 8>(a, gi, sidx, kThreads, last_flag, sum_of);
   else
     finish_strip<NB, I4, OUT_F16>(a, gi, sidx, kThreads, last_flag, sum_of);
 }
@@ -929,7 +936,7 @@ __global__ __launch_bounds__(kRingThreads, 5) void decode_ring_kernel(A a) {
            *reinterpret_cast<const f32x4_t*>(red + ((4 + f) * 64 + ln) * 4);
   };
   if constexpr (ArgTraits<A>::kEpilogue)
-    finish_strip_fused<NB, false>(a, gi, sidx, kRingThreads, last_flag, sum_of);
+    finish_strip_fused<NB, false, 4>(a, gi, sidx, kRingThreads, last_flag, sum_of);
   else
     finish_strip<NB, false, OUT_F16>(a, gi, sidx, kRingThreads, last_flag, sum_of);
 }

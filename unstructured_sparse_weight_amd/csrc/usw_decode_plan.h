@@ -62,7 +62,8 @@ constexpr int kRingDepth = 3;
 // Fewest GroupTile columns the automatic split gives a ring workgroup.
 constexpr int64_t kRingMinCols = 10;
 
-// The argument structs with an epilogue carry Y's type themselves.
+// The argument structs with an epilogue carry Y's type themselves; it is a
+// template argument where the kernel's sums go by it.
 template <class A>
 void ring_launch(const A& a, bool f16out, dim3 grid, hipStream_t s) {
   if constexpr (!ArgTraits<A>::kEpilogue) {
@@ -187,7 +188,7 @@ size_t workspace_bytes(const usw::Geometry& g, const Plan& p) {
 
 template <int NB, bool I4, int CH, class C, class A>
 void launch_cfg(const A& a, bool f16out, dim3 grid, hipStream_t s) {
-  if constexpr (!ArgTraits<A>::kEpilogue) {
+  if constexpr (!ArgTraits<A>::kEpilogue || I4) {
     if (!f16out) {
       decode_kernel<NB, I4, CH, false, C, A><<<grid, C::kThreadsPerGroup, 0, s>>>(a);
       return;

@@ -156,7 +156,7 @@ usw_status fused_impl(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_ty
     if (e.mul) a.e.mul += e.ld_mul * n0;
     if (e.res) a.e.res += e.ld_res * n0;
     const int nb = nc > 32 ? 4 : nc > 16 ? 2 : 1;
-    launch_pass(a, p.ring, i4, lean, nb, true, dim3(static_cast<unsigned>(nblk)), s);
+    launch_pass(a, p.ring, i4, lean, nb, e.f16out, dim3(static_cast<unsigned>(nblk)), s);
     if (hipGetLastError() != hipSuccess) return USW_ERR_HIP;
   }
   return USW_OK;
@@ -300,7 +300,7 @@ usw_status expert_impl(const usw_expert_fmt* f, const uint16_t* X, int32_t T, co
   a.tiles = static_cast<int>(p.tiles);
   a.lg_chunk = p.lg_chunk;
   a.Gr = static_cast<int>(g.Gr);
-  launch_pass(a, p.ring, i4, p.lean, 1 << (p.lg_chunk - 4), true, dim3(static_cast<unsigned>(p.tiles * per)),
+  launch_pass(a, p.ring, i4, p.lean, 1 << (p.lg_chunk - 4), e.f16out, dim3(static_cast<unsigned>(p.tiles * per)),
               static_cast<hipStream_t>(stream));
   return hipGetLastError() == hipSuccess ? USW_OK : USW_ERR_HIP;
 }

@@ -12,14 +12,20 @@
 // blocks before; no atomics decide an order, and equal inputs give equal
 // plans.
 //
+// A wave chooses for four tokens at a time, so that their dependent steps
+// overlap: the maximum by DPP moves, the lowest expert that has it by a ballot.
+//
 // Up to 256 tokens one workgroup does all of it in one launch, since there
 // the launches are the time.  Above, blocks of 64 tokens (one bitmap word
-// per expert) choose and count, a scan adds the counts down the blocks, and
-// the blocks place their slots.
+// per expert) choose and count, and in a second launch each block adds the
+// counts of the blocks before it and places its slots.  From 256 blocks on, where
+// every block would read a long table, a launch between them turns the counts
+// into prefixes.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "usw.h"
 #include "usw_device.h"
@@ -33,6 +39,7 @@ constexpr int kMaxRouteExperts = 1024;
 constexpr int kMaxTopK = 16;
 constexpr int kOneTokens = 256;    // tokens the one-workgroup kernel takes
 constexpr int kBlockTokens = 64;   // tokens per workgroup above that
+constexpr int kAddBlocks = 256;    // most blocks whose counts every block adds itself
 
 struct RouteArgs {
   const void* __restrict__ logits;
@@ -44,6 +51,7 @@ struct RouteArgs {
   int32_t* __restrict__ pos;       // [T][k]
   int32_t* __restrict__ counts;    // [blocks][E], then [E] totals
   int T, E, k, blocks, f16, renormalize;
+  int lg_e;                        // log2 of E rounded up to a power of two
 };
 
 // A float as an unsigned integer in the same order; NaN and -inf become 0,
@@ -61,95 +69,135 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 // exp(v - top) for a top that is the maximum: equal infinities count 1.
 __device__ __forceinline__ float exp_below(float v, float top) { return v == top ? 1.0f : expf(v - top); }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
 }
 
-// The choice of one token by one wave; PER = experts per lane.  Lane j < k
-// ends with the j-th chosen expert in *id (-1: none left) and its weight.
+// Sum over the 64 lanes, in every lane, in a fixed order.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<0x111, 0xf>(v);   // row_shr:1
+  v += dpp<0x112, 0xf>(v);   // row_shr:2
+  v += dpp<0x114, 0xf>(v);   // row_shr:4
+  v += dpp<0x118, 0xf>(v);   // row_shr:8
+  v += dpp<0x142, 0xa>(v);   // row_bcast:15
+  v += dpp<0x143, 0xc>(v);   // row_bcast:31
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+
+// The logits of a token, PER to a lane, as order keys (0 past the experts).
 template <int PER>
-__device__ __forceinline__ void choose(const RouteArgs& a, int t, int lane, int* id, float* weight) {
-  uint32_t key[PER];
+struct Keys {
+  uint32_t k[PER];
+};
+
+template <int PER>
+__device__ __forceinline__ Keys<PER> load_keys(const RouteArgs& a, int t, int lane) {
+  Keys<PER> r;
+  float v[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = lane + 64 * i;
-    key[i] = 0;
-    if (e < a.E) {
-      const int64_t at = t * a.ld + e;
-      key[i] = order_key(a.f16 ? static_cast<float>(static_cast<const _Float16*>(a.logits)[at])
-                               : static_cast<const float*>(a.logits)[at]);
-    }
+    const int64_t at = t * a.ld + min(lane + 64 * i, a.E - 1);
+    v[i] = a.f16 ? static_cast<float>(static_cast<const _Float16*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
   }
-  float top = 0.0f, total = 0.0f, mine = 0.0f;
-  int chosen = -1;
-  for (int j = 0; j < a.k; ++j) {
-    // The largest key, the lowest expert among equals: the maximum of
-    // (key, ~expert) over the lanes.
-    uint64_t best = 0;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const uint64_t c = (static_cast<uint64_t>(key[i]) << 32) | ~static_cast<uint32_t>(lane + 64 * i);
-      best = c > best ? c : best;
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      const uint64_t o = __shfl_xor(best, d);
-      best = o > best ? o : best;
-    }
-    const uint32_t bkey = static_cast<uint32_t>(best >> 32);
-    if (bkey == 0) break;
-    const int e = static_cast<int>(~static_cast<uint32_t>(best));
-    const float v = key_value(bkey);
-    if (j == 0) {
-      top = v;
-      if (!a.renormalize) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-          if (key[i]) total += exp_below(key_value(key[i]), top);
-        total = wave_sum(total);
-      }
-    }
-    const float p = exp_below(v, top);
-    if (a.renormalize) total += p;
-    if (lane == j) {
-      chosen = e;
-      mine = p;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane + 64 * i == e) key[i] = 0;
-  }
-  *id = chosen;
-  *weight = chosen >= 0 ? mine / total : 0.0f;
+  for (int i = 0; i < PER; ++i) r.k[i] = lane + 64 * i < a.E ? order_key(v[i]) : 0u;
+  return r;
 }
 
-__device__ __forceinline__ void choose_any(const RouteArgs& a, int t, int lane, int* id, float* weight) {
-  if (a.E <= 64) choose<1>(a, t, lane, id, weight);
-  else if (a.E <= 128) choose<2>(a, t, lane, id, weight);
-  else if (a.E <= 256) choose<4>(a, t, lane, id, weight);
-  else choose<16>(a, t, lane, id, weight);
+// The choices of N tokens by one wave, step by step together so that their
+// dependent moves overlap.  Lane j < k ends with the j-th chosen expert of
+// token q in id[q] (-1: none left) and its weight.
+template <int PER, int N>
+__device__ __forceinline__ void choose(const RouteArgs& a, Keys<PER> (&key)[N], int lane, int (&id)[N], float (&weight)[N]) {
+  uint32_t top[N], mine[N];
+  float all[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    uint32_t best = key[q].k[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) best = max(best, key[q].k[i]);
+    top[q] = wave_max(best);
+    all[q] = 0.0f;
+    if (!a.renormalize) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (key[q].k[i]) all[q] += exp_below(key_value(key[q].k[i]), key_value(top[q]));
+    }
+    mine[q] = 0;
+    id[q] = -1;
+  }
+  for (int j = 0; j < a.k; ++j) {
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      uint32_t best = key[q].k[0];
+#pragma unroll
+      for (int i = 1; i < PER; ++i) best = max(best, key[q].k[i]);
+      best = wave_max(best);
+      // The lowest expert that has it: expert lane + 64 i.
+      int e = -1;
+#pragma unroll
+      for (int i = PER - 1; i >= 0; --i) {
+        const uint64_t has = __ballot(key[q].k[i] == best);
+        if (has) e = 64 * i + __builtin_ctzll(has);
+      }
+      if (lane == j && best != 0) {
+        id[q] = e;
+        mine[q] = best;
+      }
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (lane + 64 * i == e) key[q].k[i] = 0;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const float p = mine[q] ? exp_below(key_value(mine[q]), key_value(top[q])) : 0.0f;
+    const float total = wave_sum(a.renormalize ? p : all[q]);
+    weight[q] = mine[q] ? p / total : 0.0f;
+  }
+}
+
+// Chooses for the block's tokens [t0, t0 + n), wave w for tokens w, w + WAVES,
+// ..., TOGETHER at a time, and sets their bits in bits.
+template <int WAVES, int PER, int TOGETHER>
+__device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n, uint32_t* bits) {
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  for (int i0 = w; i0 < n; i0 += TOGETHER * WAVES) {
+    Keys<PER> key[TOGETHER];
+    int id[TOGETHER];
+    float weight[TOGETHER];
+#pragma unroll
+    for (int q = 0; q < TOGETHER; ++q) key[q] = load_keys<PER>(a, t0 + min(i0 + q * WAVES, n - 1), lane);
+    choose<PER, TOGETHER>(a, key, lane, id, weight);
+#pragma unroll
+    for (int q = 0; q < TOGETHER; ++q) {
+      const int i = i0 + q * WAVES;
+      if (i < n && lane < a.k) {
+        const int64_t at = static_cast<int64_t>(t0 + i) * a.k + lane;
+        a.ids[at] = id[q];
+        a.weights[at] = weight[q];
+        if (id[q] >= 0) atomicOr(&bits[(i >> 5) * a.E + id[q]], 1u << (i & 31));
+      }
+    }
+  }
 }
 
 // Chooses for the block's tokens [t0, t0 + n), n <= 64 WORDS, and leaves each
-// expert's bitmap of the tokens that chose it in bits[WORDS][E].
+// expert's bitmap of the tokens that chose it in bits[2 WORDS][E].
 template <int WAVES, int WORDS>
 __device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int n, uint32_t* bits) {
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  for (int i = tid; i < 2 * WORDS * a.E; i += 64 * WAVES) bits[i] = 0u;
+  for (int i = threadIdx.x; i < 2 * WORDS * a.E; i += 64 * WAVES) bits[i] = 0u;
   __syncthreads();
-  for (int i = w; i < n; i += WAVES) {
-    int id;
-    float weight;
-    choose_any(a, t0 + i, lane, &id, &weight);
-    if (lane < a.k) {
-      const int64_t at = static_cast<int64_t>(t0 + i) * a.k + lane;
-      a.ids[at] = id;
-      a.weights[at] = weight;
-      if (id >= 0) atomicOr(&bits[(i >> 5) * a.E + id], 1u << (i & 31));
-    }
-  }
+  auto any = [&](auto together) {
+    constexpr int N = decltype(together)::value;
+    if (a.E <= 64) choose_tokens<WAVES, 1, N>(a, t0, n, bits);
+    else if (a.E <= 128) choose_tokens<WAVES, 2, N>(a, t0, n, bits);
+    else if (a.E <= 256) choose_tokens<WAVES, 4, N>(a, t0, n, bits);
+    else choose_tokens<WAVES, 16, 1>(a, t0, n, bits);
+  };
+  if (n <= WAVES) any(std::integral_constant<int, 1>{});
+  else any(std::integral_constant<int, 4>{});
   __syncthreads();
 }
 
@@ -239,19 +287,43 @@ __global__ __launch_bounds__(64) void route_scan_kernel(RouteArgs a) {
   if (lane == 0) a.counts[static_cast<int64_t>(a.blocks) * a.E + e] = static_cast<int32_t>(before);
 }
 
-__global__ __launch_bounds__(256) void route_place_kernel(RouteArgs a) {
-  extern __shared__ uint32_t lds[];   // first slots [E + 1]
+// PREFIXED: the scan has run.  Otherwise the block adds the counts of all
+// blocks, and of those before it, itself: its threads in groups of E rounded
+// up to a power of two, each group every n-th block.
+template <bool PREFIXED>
+__global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs a) {
+  extern __shared__ uint32_t lds[];   // first slots [E + 1], then [E] slots before this block
   int32_t* first = reinterpret_cast<int32_t*>(lds);
-  const int tid = threadIdx.x;
-  for (int e = tid; e < a.E; e += 256) first[e] = a.counts[static_cast<int64_t>(a.blocks) * a.E + e];
+  int32_t* before = first + a.E + 1;
+  const int tid = threadIdx.x, blk = static_cast<int>(blockIdx.x);
+  if constexpr (PREFIXED) {
+    for (int e = tid; e < a.E; e += 1024) {
+      first[e] = a.counts[static_cast<int64_t>(a.blocks) * a.E + e];
+      before[e] = a.counts[static_cast<int64_t>(blk) * a.E + e];
+    }
+  } else {
+    for (int e = tid; e < a.E; e += 1024) first[e] = before[e] = 0;
+    __syncthreads();
+    const int groups = 1024 >> a.lg_e, e = tid & ((1 << a.lg_e) - 1);
+    if (e < a.E) {
+      int all = 0, mine = 0;
+#pragma unroll 8
+      for (int b = tid >> a.lg_e; b < a.blocks; b += groups) {
+        const int c = a.counts[static_cast<int64_t>(b) * a.E + e];
+        all += c;
+        mine += b < blk ? c : 0;
+      }
+      if (all) atomicAdd(&first[e], all);       // integer sums: their order does not matter
+      if (mine) atomicAdd(&before[e], mine);
+    }
+  }
   __syncthreads();
   scan_experts(first, a.E);
-  if (blockIdx.x == 0)
-    for (int e = tid; e <= a.E; e += 256) a.slots[e] = first[e];
-  const int t0 = static_cast<int>(blockIdx.x) * kBlockTokens;
+  if (blk == 0)
+    for (int e = tid; e <= a.E; e += 1024) a.slots[e] = first[e];
+  const int t0 = blk * kBlockTokens;
   const int n = min(kBlockTokens, a.T - t0) * a.k, live = first[a.E];
-  const int32_t* before = a.counts + static_cast<int64_t>(blockIdx.x) * a.E;
-  for (int i = tid; i < n; i += 256) {
+  for (int i = tid; i < n; i += 1024) {
     const int64_t at = static_cast<int64_t>(t0) * a.k + i;
     const int id = a.ids[at];
     if (id >= 0) {
@@ -268,9 +340,9 @@ __global__ __launch_bounds__(256) void route_place_kernel(RouteArgs a) {
 // ---------------------------------------------------------------------------
 //
 // out[t] = res[t] + sum over j = 0 .. k-1, in that order, of
-// weights[t][j] * y[pos[t][j]].  Bound by the bytes of y: a thread owns eight
-// columns of one token and has the loads of up to eight slots in flight.
-
+// weights[t][j] * y[pos[t][j]].  Bound by the bytes of y: a wave owns 512
+// columns of one token, so slots and weights are scalar loads and the rows'
+// loads, up to eight in flight, go without a mask.
 struct CombineArgs {
   const void* __restrict__ y;
   const int32_t* __restrict__ pos;
@@ -278,8 +350,8 @@ struct CombineArgs {
   const uint16_t* res;
   void* out;
   int64_t ld_res;
-  int64_t total;   // T * M / 8
-  int S, M8, k;
+  int64_t waves;   // T * parts
+  int S, M8, k, parts;   // parts: waves per token
 };
 
 struct Eight {
@@ -287,54 +359,68 @@ struct Eight {
 };
 
 template <bool F16>
-__device__ __forceinline__ Eight load8(const void* p, int64_t at) {
-  Eight r;
-  if constexpr (F16) {
-    const half8_t h = *reinterpret_cast<const half8_t*>(static_cast<const _Float16*>(p) + at);
+struct Raw8;   // eight columns as they lie in memory
+template <>
+struct Raw8<true> {
+  half8_t h;
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    h = *reinterpret_cast<const half8_t*>(static_cast<const _Float16*>(p) + at);
+  }
+  __device__ __forceinline__ Eight value() const {
+    Eight r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       r.lo[i] = static_cast<float>(h[i]);
       r.hi[i] = static_cast<float>(h[4 + i]);
     }
-  } else {
-    const f32x4_t* q = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + at);
-    r.lo = q[0];
-    r.hi = q[1];
+    return r;
   }
-  return r;
-}
+};
+template <>
+struct Raw8<false> {
+  Eight v;
+  __device__ __forceinline__ void load(const void* p, int64_t at) {
+    const f32x4_t* q = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + at);
+    v.lo = q[0];
+    v.hi = q[1];
+  }
+  __device__ __forceinline__ Eight value() const { return v; }
+};
 
 template <bool Y16, bool OUT16>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= a.total) return;
-  const int64_t t = a.total <= 0xFFFFFFFFll ? static_cast<uint32_t>(i) / static_cast<uint32_t>(a.M8) : i / a.M8;
-  const int col = 8 * static_cast<int>(i - t * a.M8);
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (i >= a.waves) return;
+  const int64_t t = a.waves <= 0xFFFFFFFFll ? static_cast<uint32_t>(i) / static_cast<uint32_t>(a.parts) : i / a.parts;
+  const int unit = 64 * static_cast<int>(i - t * a.parts) + (threadIdx.x & 63);
+  if (unit >= a.M8) return;
+  const int col = 8 * unit;
   const int64_t M = 8ll * a.M8;
+  Raw8<true> r;
+  if (a.res) r.load(a.res, t * a.ld_res + col);
   Eight sum = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
   for (int j0 = 0; j0 < a.k; j0 += 8) {
-    Eight v[8];
-    float w[8];
+    Raw8<Y16> v[8];
     bool has[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t at = t * a.k + min(j0 + j, a.k - 1);
-      const int p = a.pos[at];
+      const int p = a.pos[t * a.k + min(j0 + j, a.k - 1)];
       has[j] = j0 + j < a.k && static_cast<uint32_t>(p) < static_cast<uint32_t>(a.S);
-      w[j] = a.weights[at];
-      if (has[j]) v[j] = load8<Y16>(a.y, p * M + col);
+      if (has[j]) v[j].load(a.y, p * M + col);
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (has[j]) {
-        sum.lo += w[j] * v[j].lo;
-        sum.hi += w[j] * v[j].hi;
+        const float w = a.weights[t * a.k + j0 + j];
+        const Eight e = v[j].value();
+        sum.lo += w * e.lo;
+        sum.hi += w * e.hi;
       }
   }
   if (a.res) {
-    const Eight r = load8<true>(a.res, t * a.ld_res + col);
-    sum.lo += r.lo;
-    sum.hi += r.hi;
+    const Eight e = r.value();
+    sum.lo += e.lo;
+    sum.hi += e.hi;
   }
   const int64_t o = t * M + col;
   if constexpr (OUT16) {
@@ -417,8 +503,14 @@ usw_status usw_expert_route(const void* logits, int32_t l_type, int64_t ld, int3
   } else {
     a.blocks = (T + kBlockTokens - 1) / kBlockTokens;
     route_choose_kernel<<<a.blocks, 1024, 2 * E * sizeof(uint32_t), s>>>(a);
-    route_scan_kernel<<<E, 64, 0, s>>>(a);
-    route_place_kernel<<<a.blocks, 256, (E + 1) * sizeof(uint32_t), s>>>(a);
+    const size_t lds = (2 * E + 1) * sizeof(uint32_t);
+    while ((1 << a.lg_e) < E) ++a.lg_e;
+    if (a.blocks > kAddBlocks) {
+      route_scan_kernel<<<E, 64, 0, s>>>(a);
+      route_place_kernel<true><<<a.blocks, 1024, lds, s>>>(a);
+    } else {
+      route_place_kernel<false><<<a.blocks, 1024, lds, s>>>(a);
+    }
   }
   return hipGetLastError() == hipSuccess ? USW_OK : USW_ERR_HIP;
 }
@@ -447,8 +539,9 @@ usw_status usw_expert_combine(const void* Y, int32_t y_type, int32_t S, int32_t 
   a.S = S;
   a.M8 = M / 8;
   a.k = k;
-  a.total = static_cast<int64_t>(T) * a.M8;
-  const int64_t blocks = (a.total + 255) / 256;
+  a.parts = (a.M8 + 63) / 64;
+  a.waves = static_cast<int64_t>(T) * a.parts;
+  const int64_t blocks = (a.waves + 3) / 4;
   if (blocks >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
   const dim3 grid(static_cast<unsigned>(blocks));
   hipStream_t s = static_cast<hipStream_t>(stream);

@@ -585,22 +585,29 @@ WidePlan wide_plan(const Geometry& g, int32_t E, int32_t S) {
     const int64_t n = p.group == 1 ? (S + kBN[t] - 1) / kBN[t] : std::max<int64_t>(runs, S / kBN[t] + runs / 2);
     return n * ((g.M + kBM[t] - 1) / kBM[t]);
   };
-  // Large tiles from one whole round on; they are the fastest on the matrix
-  // cores (MI355X, fp16, expansion included: 4096^3 131 us against 174 with
-  // medium tiles, 11008x4096 N = 2048 221 / 243), but with fewer tiles too
-  // many columns are shared (11008x4096 N = 512: 99 / 88, 5120x2560 N = 1400:
-  // 77 / 58).  Small tiles up to 4e9 multiply-adds, where the grid is short of
-  // workgroups (1152x1152 N = 300: 13.2 us against 17.1 with medium tiles,
-  // 4096x4096 N = 100 26.2 / 30.4; 5120x5120 N = 200 40.5 / 40.9, N = 300
-  // 50.1 / 44.3).
-  p.tiling = expected(0) >= kComputeUnits ? 0 : g.M * g.K * S <= 4000000000ll ? 2 : 1;
+  // Large tiles are the fastest on the matrix cores, but need a whole round
+  // of them, and each stands alone on its compute unit: nothing hides its
+  // fill and epilogue, nor the sums of the columns shared after the last
+  // whole round.  In microseconds of MI355X, fitted to the times below: 1.82 a
+  // column and 6 a tile, 35 where tiles are left over, against 0.64 a column
+  // of a medium tile.  Expansion included, large / medium: 4096^3 131 / 174,
+  // 8192x4096 N = 2048 126 / 147, 20480x2560 N = 2000 224 / 257, 11904x1152
+  // N = 2000 108 / 72, 8 experts of 4096x2048 with 500 rows each 155 / 120.
+  // Small tiles up to 4e9 multiply-adds, where the grid is short of workgroups,
+  // small / medium: 1152x1152 N = 300 13.2 / 17.1, 4096x4096 N = 100 26.2 /
+  // 30.4; 5120x5120 N = 200 40.5 / 40.9, N = 300 50.1 / 44.3.
+  const int64_t large = expected(0), rounds = large / kComputeUnits;
+  const double large_us = 1.82 * large * g.Gc / kComputeUnits + 6.0 * rounds + (large % kComputeUnits ? 35.0 : 0.0);
+  const double medium_us = 0.64 * expected(1) * g.Gc / kComputeUnits;
+  p.tiling = rounds > 0 && large_us < medium_us ? 0 : g.M * g.K * S <= 4000000000ll ? 2 : 1;
   // Splits of the columns, at least eight each, while they fill the chip: up
   // to 256 medium workgroups (4096x11008 N = 512: 2 splits 81.4 us, 1 113.7, 4
   // 87.7) or 704 small ones (2560x2560 N = 160: 4 splits 21.3, 1 27.3;
-  // 2048x2048 N = 70: 4 splits 15.8, 1 19.9).
+  // 2048x2048 N = 70: 4 splits 15.8, 1 19.9; 128x16064 N = 669: 16 splits 25.4,
+  // 8 26.0, 32 33.1).
   p.splits = 1;
   const int64_t most = p.tiling == 0 ? 0 : p.tiling == 1 ? 256 : 704;
-  while (p.splits < 8 && expected(p.tiling) * p.splits * 2 <= most && g.Gc >= 16 * p.splits) p.splits *= 2;
+  while (p.splits < 16 && expected(p.tiling) * p.splits * 2 <= most && g.Gc >= 16 * p.splits) p.splits *= 2;
   const int64_t mt = (g.M + kBM[p.tiling] - 1) / kBM[p.tiling];
   p.tiles = (runs + (S - runs) / kBN[p.tiling]) * mt;
   const size_t slot = static_cast<size_t>(4) * kBM[p.tiling] * kBN[p.tiling];
