@@ -673,7 +673,7 @@ usw_status usw_spmm_fused_workspace(const usw_fmt* fmt, int32_t N, int32_t split
  * else that the call reads.
  * Errors: as usw_spmm_ex, and BAD_DTYPE (act), BAD_SHAPE (a stride below M or
  * above 2^20, reserved), MISALIGNED (scales, bias, mul or res not 16-byte
- * aligned, a stride that is no multiple of 8).
+ * aligned, a stride that is no multiple of 8), UNSUPPORTED (M > 2^22).
  */
 usw_status usw_spmm_fused(const usw_fmt* fmt, const uint16_t* X, void* Y, int32_t y_type, int32_t N,
                           const usw_epilogue* ep, int32_t splits, void* ws, size_t ws_bytes, void* stream);

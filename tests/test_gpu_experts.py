@@ -167,6 +167,29 @@ def test_expanded_tilings(counts, M, K, what, val):
         near(y[torch.from_numpy(r).to(DEV)], want, bound, f"{what}, expert {e}")
 
 
+def test_weights_expanded_in_groups():
+    """More weights than are expanded at a time (1 GiB of fragments): the same
+    encoding in every place, so each expert's rows have one reference."""
+    E, M, K = 36, 4096, 4096
+    rng = np.random.default_rng(120)
+    W, mask = wl.weight_dyadic(M, K, rng), wl.mask_bernoulli(M, K, 0.5, rng)
+    enc = usw.encode(W, mask, device=DEV)
+    bank = usw.expert_bank([enc] * E)
+    counts = [240 + (e % 5) for e in range(E)]
+    counts[3], counts[17], counts[35] = 0, 900, 1
+    slots = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    S = int(slots[-1])
+    x = gpu(wl.activations_small_int(S, K, rng))
+    say("[experts] groups")
+    y = usw.expert_spmm(bank, x, gpu(slots), out_dtype=torch.float32)
+    want = usw.spmm_fused(enc, x, out_dtype=torch.float32)      # exact sums: one weight for all rows
+    assert torch.equal(y, want)
+    r = rng.integers(0, S, 20)
+    Wd = np.where(mask, W, np.float16(0)).astype(np.float64)
+    assert np.array_equal(y[torch.from_numpy(r).to(DEV)].cpu().numpy().astype(np.float64),
+                          x.cpu().numpy()[r].astype(np.float64) @ Wd.T)
+
+
 def test_long_rows_split_k_twice_the_same():
     """Few slots and long rows: several workgroups a strip; two calls give the
     same bits."""

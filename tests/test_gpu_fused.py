@@ -267,6 +267,33 @@ def test_two_streams():
         assert all(torch.equal(y, w) for y in ys)
 
 
+def test_two_threads_on_one_stream():
+    """Calls of two threads on the current stream, one with partial sums and
+    one with an expanded weight, share the stream's workspace."""
+    import threading
+    say("[fused] threads")
+    cases = []
+    for i, (M, K, N) in enumerate([(128, 5120, 9), (256, 512, 300), (512, 2048, 200)]):
+        enc, _ = weight(M, K, 0.5, "f16", 235 + i)
+        cases.append((enc, gpu(half(np.random.default_rng(236 + i), N, K))))
+    want = [usw.spmm_fused(e, x, act="silu") for e, x in cases]
+    torch.cuda.synchronize()
+    got = [[] for _ in cases]
+
+    def work(i):
+        for _ in range(30):
+            got[i].append(usw.spmm_fused(*cases[i], act="silu"))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(cases))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for ys, w in zip(got, want):
+        assert len(ys) == 30 and all(torch.equal(y, w) for y in ys)
+
+
 def test_ffn_chain():
     """OPT's and Llama's feed-forward blocks from these calls, against the
     same blocks in 64 bits with the hidden activations rounded to fp16 as the

@@ -26,6 +26,8 @@ constexpr int kMaxExperts = 1024;
 // Longest stride of the epilogue's operands, and most outputs of an expanded
 // weight: the expanded product addresses a tile's rows with 32 bits.
 constexpr int64_t kMaxLd = int64_t(1) << 20;
+// Most outputs of a weight: a pass addresses its partial sums with 32 bits.
+constexpr int64_t kMaxM = int64_t(1) << 22;
 
 // Checks an epilogue for rows of M outputs and fills the kernels' copy.
 usw_status make_epilogue(const usw_epilogue* ep, int64_t M, int32_t y_type, Epilogue* e) {
@@ -107,6 +109,7 @@ usw_status fused_impl(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_ty
   Epilogue e;
   st = make_epilogue(ep, g.M, y_type, &e);
   if (st) return st;
+  if (g.M > kMaxM) return USW_ERR_UNSUPPORTED;
   const FusedPlan c = plan_fused(f, g, N, splits_req);
   if (c.need > 0) {
     if (!ws || ws_bytes < c.need) return USW_ERR_WORKSPACE;
@@ -181,7 +184,7 @@ usw_status check_expert(const usw_expert_fmt* f, int32_t y_type, int32_t S, usw:
   usw_status st = usw::make_geometry(f->M, f->K, kGT, kGT, g);
   if (st) return st;
   if (f->E < 1 || f->reserved != 0) return USW_ERR_BAD_SHAPE;
-  if (f->E > kMaxExperts) return USW_ERR_UNSUPPORTED;
+  if (f->E > kMaxExperts || g->M > kMaxM) return USW_ERR_UNSUPPORTED;
   if (f->val_type != USW_VAL_F16 && f->val_type != USW_VAL_I4) return USW_ERR_BAD_DTYPE;
   if (y_type != USW_OUT_F16 && y_type != USW_OUT_F32) return USW_ERR_BAD_DTYPE;
   if (S < 0) return USW_ERR_BAD_N;

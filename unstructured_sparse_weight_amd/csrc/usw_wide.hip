@@ -352,7 +352,7 @@ __global__ __launch_bounds__(C::kThreads, 2) void wide_kernel(WideArgs a) {
   // share their operands in its L2.
   const int tiles = a.slots
                         ? scan_runs<C::BN>(a, lane, [](int, int, uint32_t, uint32_t, int, int) { return false; })
-                        : (a.S + C::BN - 1) / C::BN * a.mt;
+                        : static_cast<int>((static_cast<uint32_t>(a.S) + C::BN - 1) / C::BN) * a.mt;
   const int b = static_cast<int>(blockIdx.x);
   int L;
   // Streaming: R rounds of whole tiles; the U units (tile, column) from B on,
@@ -651,9 +651,9 @@ usw_status wide_launch(const WideCall& c, const Geometry& g, const WidePlan& p, 
   a.T = c.T;
   a.i4 = c.val_type == USW_VAL_I4;
   a.splits = p.splits;
+  if (p.tiles * p.splits >= (int64_t(1) << 31) || g.ngt / kExpandWaves >= (int64_t(1) << 31) - 1) return USW_ERR_UNSUPPORTED;
   const unsigned gx = static_cast<unsigned>((g.ngt + kExpandWaves - 1) / kExpandWaves);
   const int64_t blocks = p.tiling == 0 ? kComputeUnits : (p.tiles * p.splits + 7) / 8 * 8;
-  if (blocks >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
   const dim3 wgrid(static_cast<unsigned>(blocks));
   for (int e0 = 0; e0 < c.E; e0 += p.group) {
     const int e1 = std::min(c.E, e0 + p.group);

@@ -17,6 +17,7 @@ own, in the graph's memory pool.
 from __future__ import annotations
 
 import ctypes
+import threading
 from dataclasses import dataclass
 from functools import lru_cache
 
@@ -126,6 +127,9 @@ def _on(device, stream, body):
 
 
 _WS = {}   # (device index, raw stream) -> [workspace, its leading bytes that are zero between calls]
+# Held from taking a workspace until the call is enqueued: two threads on one
+# stream share it, and a call's launches must stay together.
+_LOCK = threading.Lock()
 
 
 def _workspace(device, handle, nbytes, counter_bytes):
@@ -239,9 +243,13 @@ def spmm_fused(enc, x, bias=None, act: str = "none", mul=None, residual=None, y=
         out = _output(y, (N, M), out_dtype, dev)
         yt = _out_type(out.dtype, "y")
         need, cb = _fused_sizes(M, enc.K, enc.gt_m, enc.gt_k, enc.val_type, enc.nnz, N, splits)
-        ws = _workspace(dev, handle, need, cb) if need else None
-        check(lib().usw_spmm_fused(ctypes.byref(enc.fmt()), xc.data_ptr(), out.data_ptr(), yt, N, ctypes.byref(ep),
-                                   splits, ws.data_ptr() if need else None, need, handle), "usw_spmm_fused")
+        args = ctypes.byref(enc.fmt()), xc.data_ptr(), out.data_ptr(), yt, N, ctypes.byref(ep), splits
+        if need:
+            with _LOCK:
+                ws = _workspace(dev, handle, need, cb)
+                check(lib().usw_spmm_fused(*args, ws.data_ptr(), need, handle), "usw_spmm_fused")
+        else:
+            check(lib().usw_spmm_fused(*args, None, 0, handle), "usw_spmm_fused")
         return out
 
     return _on(dev, stream, body)
@@ -289,11 +297,14 @@ def expert_spmm(bank: ExpertBank, x, offsets, rows=None, bias=None, act: str = "
         out = _output(y, (S, M), out_dtype, dev)
         yt = _out_type(out.dtype, "y")
         need, cb = _expert_sizes(bank.E, M, bank.K, bank.val_type, bank.nnz, bank.values.numel(), S)
-        ws = _workspace(dev, handle, need, cb) if need else None
-        check(lib().usw_expert_spmm(ctypes.byref(bank.fmt()), xc.data_ptr(), T, off.data_ptr(),
-                                    at.data_ptr() if at is not None else None, S, out.data_ptr(), yt,
-                                    ctypes.byref(ep), ws.data_ptr() if need else None, need, handle),
-              "usw_expert_spmm")
+        args = (ctypes.byref(bank.fmt()), xc.data_ptr(), T, off.data_ptr(), at.data_ptr() if at is not None else None,
+                S, out.data_ptr(), yt, ctypes.byref(ep))
+        if need:
+            with _LOCK:
+                ws = _workspace(dev, handle, need, cb)
+                check(lib().usw_expert_spmm(*args, ws.data_ptr(), need, handle), "usw_expert_spmm")
+        else:
+            check(lib().usw_expert_spmm(*args, None, 0, handle), "usw_expert_spmm")
         return out
 
     return _on(dev, stream, body)
