@@ -719,7 +719,7 @@ usw_status usw_expert_spmm(const usw_expert_fmt* fmt, const uint16_t* X, int32_t
                            const int32_t* rows, int32_t S, void* Y, int32_t y_type, const usw_epilogue* ep, void* ws,
                            size_t ws_bytes, void* stream);
 
-/* Workspace of usw_expert_route (need not be initialised; 0 up to 256 tokens). */
+/* Workspace of usw_expert_route (need not be initialised; may be 0). */
 usw_status usw_expert_route_workspace(int32_t T, int32_t E, int32_t k, size_t* bytes);
 
 /*

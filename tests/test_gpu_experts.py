@@ -249,6 +249,18 @@ def test_route(T, E, k, dtype):
     assert torch.all(plan.ids[::5] == -1) and torch.all(plan.weights[::5] == 0)
 
 
+@pytest.mark.parametrize("E", [2, 16, 17, 32, 33, 64, 65, 128, 129, 256, 257, 512, 513, 1000])
+def test_route_lane_layouts(E):
+    """Both layouts of a token over lanes, full and partly filled, at each number of logits to a lane."""
+    gen = torch.Generator(device=DEV).manual_seed(E)
+    for T in (2, 16, 17, 63, 64, 66):
+        say(f"[experts] route layouts T={T} E={E}")
+        logits = torch.randn(T, E, device=DEV, generator=gen)
+        logits[:, E // 2:] = logits[:, :E - E // 2]   # every value twice
+        check_route(logits, min(E, 16), False, "twice the same")
+        check_route(logits.half(), min(E, 3), True, "half")
+
+
 def test_route_all_masked_and_strided():
     logits = torch.full((300, 8), -float("inf"), device=DEV)
     say("[experts] route all masked")

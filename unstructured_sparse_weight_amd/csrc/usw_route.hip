@@ -12,20 +12,21 @@
 // blocks before; no atomics decide an order, and equal inputs give equal
 // plans.
 //
-// A wave chooses for four tokens at a time, so that their dependent steps
-// overlap: the maximum by DPP moves, the lowest expert that has it by a ballot.
+// Choosing is bound by the instructions it issues: k rounds of a maximum over
+// the experts, the lowest expert that has it, and its removal.  Four tokens
+// share a wave, 16 lanes (a DPP row) to a token, so that the moves across lanes
+// serve four tokens each.
 //
-// Up to 256 tokens one workgroup does all of it in one launch, since there
-// the launches are the time.  Above, blocks of 64 tokens (one bitmap word
-// per expert) choose and count, and in a second launch each block adds the
-// counts of the blocks before it and places its slots.  From 256 blocks on, where
-// every block would read a long table, a launch between them turns the counts
-// into prefixes.
+// Up to 64 tokens one workgroup does all of it in one launch, since there
+// the launches are the time (64 experts, k 8, 64 tokens: 5.0 us, a second
+// launch adds 2).  Above, blocks of 64 tokens choose and count, and in a second
+// launch each block adds the counts of the blocks before it and places its
+// slots.  From 256 blocks on, where every block would read a long table, a
+// launch between them turns the counts into prefixes.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
-#include <type_traits>
 
 #include "usw.h"
 #include "usw_device.h"
@@ -37,7 +38,7 @@ using namespace usw_dev;
 
 constexpr int kMaxRouteExperts = 1024;
 constexpr int kMaxTopK = 16;
-constexpr int kOneTokens = 256;    // tokens the one-workgroup kernel takes
+constexpr int kOneTokens = 64;    // tokens the one-workgroup kernel takes
 constexpr int kBlockTokens = 64;   // tokens per workgroup above that
 constexpr int kAddBlocks = 256;    // most blocks whose counts every block adds itself
 
@@ -70,142 +71,127 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 __device__ __forceinline__ float exp_below(float v, float top) { return v == top ? 1.0f : expf(v - top); }
 
 template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp(float v) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, ROWS, 0xf, false));
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, ROWS, 0xf, false));
 }
 
-// Sum over the 64 lanes, in every lane, in a fixed order.
-__device__ __forceinline__ float wave_sum(float v) {
-  v += dpp<0x111, 0xf>(v);   // row_shr:1
-  v += dpp<0x112, 0xf>(v);   // row_shr:2
-  v += dpp<0x114, 0xf>(v);   // row_shr:4
-  v += dpp<0x118, 0xf>(v);   // row_shr:8
-  v += dpp<0x142, 0xa>(v);   // row_bcast:15
-  v += dpp<0x143, 0xc>(v);   // row_bcast:31
-  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+__device__ __forceinline__ float as_float(uint32_t v) { return __builtin_bit_cast(float, v); }
+__device__ __forceinline__ uint32_t as_bits(float v) { return __builtin_bit_cast(uint32_t, v); }
+
+// Maximum and sum over the L lanes of a token, in each of them.  Over 16 lanes
+// by rotations of a DPP row: every lane adds the same pairs, so all have the
+// same sum.
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (L == 64) {
+    return wave_max(v);
+  } else {
+    v = max(v, dpp<0x128, 0xf>(v));   // row_ror:8, 4, 2, 1
+    v = max(v, dpp<0x124, 0xf>(v));
+    v = max(v, dpp<0x122, 0xf>(v));
+    return max(v, dpp<0x121, 0xf>(v));
+  }
 }
-
-// The logits of a token, PER to a lane, as order keys (0 past the experts).
-template <int PER>
-struct Keys {
-  uint32_t k[PER];
-};
-
-template <int PER>
-__device__ __forceinline__ Keys<PER> load_keys(const RouteArgs& a, int t, int lane) {
-  Keys<PER> r;
-  float v[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int64_t at = t * a.ld + min(lane + 64 * i, a.E - 1);
-    v[i] = a.f16 ? static_cast<float>(static_cast<const _Float16*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
-  }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) r.k[i] = lane + 64 * i < a.E ? order_key(v[i]) : 0u;
-  return r;
-}
-
-// The choices of N tokens by one wave, step by step together so that their
-// dependent moves overlap.  Lane j < k ends with the j-th chosen expert of
-// token q in id[q] (-1: none left) and its weight.
-template <int PER, int N>
-__device__ __forceinline__ void choose(const RouteArgs& a, Keys<PER> (&key)[N], int lane, int (&id)[N], float (&weight)[N]) {
-  uint32_t top[N], mine[N];
-  float all[N];
-#pragma unroll
-  for (int q = 0; q < N; ++q) {
-    uint32_t best = key[q].k[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i) best = max(best, key[q].k[i]);
-    top[q] = wave_max(best);
-    all[q] = 0.0f;
-    if (!a.renormalize) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (key[q].k[i]) all[q] += exp_below(key_value(key[q].k[i]), key_value(top[q]));
-    }
-    mine[q] = 0;
-    id[q] = -1;
-  }
-  for (int j = 0; j < a.k; ++j) {
-#pragma unroll
-    for (int q = 0; q < N; ++q) {
-      uint32_t best = key[q].k[0];
-#pragma unroll
-      for (int i = 1; i < PER; ++i) best = max(best, key[q].k[i]);
-      best = wave_max(best);
-      // The lowest expert that has it: expert lane + 64 i.
-      int e = -1;
-#pragma unroll
-      for (int i = PER - 1; i >= 0; --i) {
-        const uint64_t has = __ballot(key[q].k[i] == best);
-        if (has) e = 64 * i + __builtin_ctzll(has);
-      }
-      if (lane == j && best != 0) {
-        id[q] = e;
-        mine[q] = best;
-      }
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (lane + 64 * i == e) key[q].k[i] = 0;
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < N; ++q) {
-    const float p = mine[q] ? exp_below(key_value(mine[q]), key_value(top[q])) : 0.0f;
-    const float total = wave_sum(a.renormalize ? p : all[q]);
-    weight[q] = mine[q] ? p / total : 0.0f;
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (L == 64) {
+    v += as_float(dpp<0x111, 0xf>(as_bits(v)));   // row_shr:1, 2, 4, 8
+    v += as_float(dpp<0x112, 0xf>(as_bits(v)));
+    v += as_float(dpp<0x114, 0xf>(as_bits(v)));
+    v += as_float(dpp<0x118, 0xf>(as_bits(v)));
+    v += as_float(dpp<0x142, 0xa>(as_bits(v)));   // row_bcast:15, 31
+    v += as_float(dpp<0x143, 0xc>(as_bits(v)));
+    return as_float(__builtin_amdgcn_readlane(as_bits(v), 63));
+  } else {
+    v += as_float(dpp<0x128, 0xf>(as_bits(v)));
+    v += as_float(dpp<0x124, 0xf>(as_bits(v)));
+    v += as_float(dpp<0x122, 0xf>(as_bits(v)));
+    return v + as_float(dpp<0x121, 0xf>(as_bits(v)));
   }
 }
 
-// Chooses for the block's tokens [t0, t0 + n), wave w for tokens w, w + WAVES,
-// ..., TOGETHER at a time, and sets their bits in bits.
-template <int WAVES, int PER, int TOGETHER>
+// Chooses for the block's tokens [t0, t0 + n), L lanes to a token and PER
+// logits to a lane (expert c + L i), and sets their bits in bits.
+template <int WAVES, int L, int PER>
 __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n, uint32_t* bits) {
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  for (int i0 = w; i0 < n; i0 += TOGETHER * WAVES) {
-    Keys<PER> key[TOGETHER];
-    int id[TOGETHER];
-    float weight[TOGETHER];
+  const int c = threadIdx.x & (L - 1);
+  for (int i = threadIdx.x / L; i - static_cast<int>(threadIdx.x & 63) / L < n; i += 64 * WAVES / L) {
+    const int64_t row = (t0 + min(i, n - 1)) * a.ld;
+    float v[PER];
 #pragma unroll
-    for (int q = 0; q < TOGETHER; ++q) key[q] = load_keys<PER>(a, t0 + min(i0 + q * WAVES, n - 1), lane);
-    choose<PER, TOGETHER>(a, key, lane, id, weight);
+    for (int q = 0; q < PER; ++q) {
+      const int64_t at = row + min(c + L * q, a.E - 1);
+      v[q] = a.f16 ? static_cast<float>(static_cast<const _Float16*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
+    }
+    uint32_t key[PER], top = 0, mine = 0;
+    float all = 0.0f;
+    int id = -1;
 #pragma unroll
-    for (int q = 0; q < TOGETHER; ++q) {
-      const int i = i0 + q * WAVES;
-      if (i < n && lane < a.k) {
-        const int64_t at = static_cast<int64_t>(t0 + i) * a.k + lane;
-        a.ids[at] = id[q];
-        a.weights[at] = weight[q];
-        if (id[q] >= 0) atomicOr(&bits[(i >> 5) * a.E + id[q]], 1u << (i & 31));
+    for (int q = 0; q < PER; ++q) key[q] = c + L * q < a.E ? order_key(v[q]) : 0u;
+    for (int j = 0; j < a.k; ++j) {
+      uint32_t best = key[0];
+#pragma unroll
+      for (int q = 1; q < PER; ++q) best = max(best, key[q]);
+      best = lanes_max<L>(best);
+      if (j == 0) {
+        top = best;
+        if (!a.renormalize) {
+#pragma unroll
+          for (int q = 0; q < PER; ++q)
+            if (key[q]) all += exp_below(key_value(key[q]), key_value(top));
+        }
       }
+      // The lowest expert that has it, as the largest complement.
+      uint32_t at = 0;
+#pragma unroll
+      for (int q = PER - 1; q >= 0; --q) at = key[q] == best ? ~static_cast<uint32_t>(L * q) - c : at;
+      const int e = static_cast<int>(~lanes_max<L>(at));
+      if (c == j && best != 0) {
+        id = e;
+        mine = best;
+      }
+#pragma unroll
+      for (int q = 0; q < PER; ++q) key[q] = e - c == L * q ? 0u : key[q];
+    }
+    const float p = mine ? exp_below(key_value(mine), key_value(top)) : 0.0f;
+    const float total = lanes_sum<L>(a.renormalize ? p : all);
+    if (i < n && c < a.k) {
+      const int64_t at = static_cast<int64_t>(t0 + i) * a.k + c;
+      a.ids[at] = id;
+      a.weights[at] = mine ? p / total : 0.0f;
+      if (id >= 0) atomicOr(&bits[(i >> 5) * a.E + id], 1u << (i & 31));
     }
   }
 }
 
-// Chooses for the block's tokens [t0, t0 + n), n <= 64 WORDS, and leaves each
-// expert's bitmap of the tokens that chose it in bits[2 WORDS][E].
-template <int WAVES, int WORDS>
+// Chooses for the block's tokens [t0, t0 + n), n <= 64, and leaves each
+// expert's bitmap of the tokens that chose it in bits[2][E].
+template <int WAVES>
 __device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int n, uint32_t* bits) {
-  for (int i = threadIdx.x; i < 2 * WORDS * a.E; i += 64 * WAVES) bits[i] = 0u;
+  for (int i = threadIdx.x; i < 2 * a.E; i += 64 * WAVES) bits[i] = 0u;
   __syncthreads();
-  auto any = [&](auto together) {
-    constexpr int N = decltype(together)::value;
-    if (a.E <= 64) choose_tokens<WAVES, 1, N>(a, t0, n, bits);
-    else if (a.E <= 128) choose_tokens<WAVES, 2, N>(a, t0, n, bits);
-    else if (a.E <= 256) choose_tokens<WAVES, 4, N>(a, t0, n, bits);
-    else choose_tokens<WAVES, 16, 1>(a, t0, n, bits);
-  };
-  if (n <= WAVES) any(std::integral_constant<int, 1>{});
-  else any(std::integral_constant<int, 4>{});
+  // 16 lanes to a token issue the fewest instructions (64 tokens, 256 experts,
+  // k 8: 9.3 us against 13.4 with 64 lanes), 64 lanes have the shorter chain
+  // where one token is all a wave has (1 token: 4.3 us against 5.9).  Above 512
+  // experts the two are equal at 64 tokens, and 64 lanes keep fewer registers.
+  if (a.E > 512) choose_tokens<WAVES, 64, 16>(a, t0, n, bits);
+  else if (n <= WAVES && a.E > 64) {
+    if (a.E <= 128) choose_tokens<WAVES, 64, 2>(a, t0, n, bits);
+    else if (a.E <= 256) choose_tokens<WAVES, 64, 4>(a, t0, n, bits);
+    else choose_tokens<WAVES, 64, 8>(a, t0, n, bits);
+  } else if (a.E <= 16) choose_tokens<WAVES, 16, 1>(a, t0, n, bits);
+  else if (a.E <= 32) choose_tokens<WAVES, 16, 2>(a, t0, n, bits);
+  else if (a.E <= 64) choose_tokens<WAVES, 16, 4>(a, t0, n, bits);
+  else if (a.E <= 128) choose_tokens<WAVES, 16, 8>(a, t0, n, bits);
+  else if (a.E <= 256) choose_tokens<WAVES, 16, 16>(a, t0, n, bits);
+  else choose_tokens<WAVES, 16, 32>(a, t0, n, bits);
   __syncthreads();
 }
 
 // Tokens of the block before token i that chose expert e.
 __device__ __forceinline__ int rank_in(const uint32_t* bits, int E, int e, int i) {
-  int r = __builtin_popcount(bits[(i >> 5) * E + e] & ((1u << (i & 31)) - 1u));
-  for (int q = 0; q < (i >> 5); ++q) r += __builtin_popcount(bits[q * E + e]);
-  return r;
+  const int r = __builtin_popcount(bits[(i >> 5) * E + e] & ((1u << (i & 31)) - 1u));
+  return i >> 5 ? r + __builtin_popcount(bits[e]) : r;
 }
 
 // Exclusive prefix of v[0 .. E) in place by the first wave, v[E] = the total.
@@ -225,16 +211,13 @@ __device__ __forceinline__ void scan_experts(int32_t* v, int E) {
 }
 
 __global__ __launch_bounds__(1024) void route_one_kernel(RouteArgs a) {
-  extern __shared__ uint32_t lds[];   // bits [8][E], first slots [E + 1]
+  extern __shared__ uint32_t lds[];   // bits [2][E], first slots [E + 1]
   uint32_t* bits = lds;
-  int32_t* first = reinterpret_cast<int32_t*>(lds + 8 * a.E);
+  int32_t* first = reinterpret_cast<int32_t*>(lds + 2 * a.E);
   const int tid = threadIdx.x;
-  choose_block<16, 4>(a, 0, a.T, bits);
+  choose_block<16>(a, 0, a.T, bits);
   for (int e = tid; e < a.E; e += 1024) {
-    int c = 0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) c += __builtin_popcount(bits[q * a.E + e]);
-    first[e] = c;
+    first[e] = __builtin_popcount(bits[e]) + __builtin_popcount(bits[a.E + e]);
   }
   __syncthreads();
   scan_experts(first, a.E);
@@ -260,7 +243,7 @@ __global__ __launch_bounds__(1024) void route_choose_kernel(RouteArgs a) {
   extern __shared__ uint32_t lds[];   // bits [2][E]
   const int t0 = static_cast<int>(blockIdx.x) * kBlockTokens;
   const int n = min(kBlockTokens, a.T - t0);
-  choose_block<16, 1>(a, t0, n, lds);
+  choose_block<16>(a, t0, n, lds);
   const int tid = threadIdx.x;
   for (int e = tid; e < a.E; e += 1024)
     a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = __builtin_popcount(lds[e]) + __builtin_popcount(lds[a.E + e]);
@@ -499,7 +482,7 @@ usw_status usw_expert_route(const void* logits, int32_t l_type, int64_t ld, int3
   a.renormalize = renormalize != 0;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (T <= kOneTokens) {
-    route_one_kernel<<<1, 1024, (9 * E + 1) * sizeof(uint32_t), s>>>(a);
+    route_one_kernel<<<1, 1024, (3 * E + 1) * sizeof(uint32_t), s>>>(a);
   } else {
     a.blocks = (T + kBlockTokens - 1) / kBlockTokens;
     route_choose_kernel<<<a.blocks, 1024, 2 * E * sizeof(uint32_t), s>>>(a);
