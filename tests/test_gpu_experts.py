@@ -261,6 +261,16 @@ def test_route_lane_layouts(E):
         check_route(logits.half(), min(E, 3), True, "half")
 
 
+@pytest.mark.parametrize("T,E,k", [(4096, 33, 3), (4097, 9, 2), (16384, 5, 2), (16389, 130, 8), (20000, 3, 1)])
+def test_route_many_tokens(T, E, k):
+    """Each size of a block of tokens, and the prefixes made by a launch of their own."""
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    say(f"[experts] route many tokens T={T} E={E}")
+    logits = torch.randn(T, E, device=DEV, generator=gen).half()
+    logits[T // 3:T // 2] = -float("inf")
+    check_route(logits, k, True, "many tokens")
+
+
 def test_route_all_masked_and_strided():
     logits = torch.full((300, 8), -float("inf"), device=DEV)
     say("[experts] route all masked")

@@ -19,7 +19,7 @@
 //
 // Up to 64 tokens one workgroup does all of it in one launch, since there
 // the launches are the time (64 experts, k 8, 64 tokens: 5.0 us, a second
-// launch adds 2).  Above, blocks of 64 tokens choose and count, and in a second
+// launch adds 2).  Above, blocks of tokens choose and count, and in a second
 // launch each block adds the counts of the blocks before it and places its
 // slots.  From 256 blocks on, where every block would read a long table, a
 // launch between them turns the counts into prefixes.
@@ -38,8 +38,8 @@ using namespace usw_dev;
 
 constexpr int kMaxRouteExperts = 1024;
 constexpr int kMaxTopK = 16;
-constexpr int kOneTokens = 64;    // tokens the one-workgroup kernel takes
-constexpr int kBlockTokens = 64;   // tokens per workgroup above that
+constexpr int kOneTokens = 64;     // tokens the one-workgroup kernel takes
+constexpr int kFineTokens = 4096;  // above that, blocks of 32 tokens up to here, then of 64
 constexpr int kAddBlocks = 256;    // most blocks whose counts every block adds itself
 
 struct RouteArgs {
@@ -52,8 +52,14 @@ struct RouteArgs {
   int32_t* __restrict__ pos;       // [T][k]
   int32_t* __restrict__ counts;    // [blocks][E], then [E] totals
   int T, E, k, blocks, f16, renormalize;
+  int per;                         // tokens to a block
   int lg_e;                        // log2 of E rounded up to a power of two
 };
+
+// Blocks of 32 tokens choose sooner (256 experts, k 8, 256 tokens: 9.5 us
+// against 11.8), but leave twice the counts to add (512 experts, k 2, 4000
+// tokens: 15.1 us against 14.6, and the table grows with the square of T).
+constexpr int block_tokens(int32_t T) { return T <= kFineTokens ? 32 : 64; }
 
 // A float as an unsigned integer in the same order; NaN and -inf become 0,
 // which is below every value that can be chosen.
@@ -164,11 +170,11 @@ __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n,
   }
 }
 
-// Chooses for the block's tokens [t0, t0 + n), n <= 64, and leaves each
-// expert's bitmap of the tokens that chose it in bits[2][E].
+// Chooses for the block's tokens [t0, t0 + n), n <= 4 WAVES, and leaves each
+// expert's bitmap of the tokens that chose it in bits[WAVES / 8][E].
 template <int WAVES>
 __device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int n, uint32_t* bits) {
-  for (int i = threadIdx.x; i < 2 * a.E; i += 64 * WAVES) bits[i] = 0u;
+  for (int i = threadIdx.x; i < WAVES / 8 * a.E; i += 64 * WAVES) bits[i] = 0u;
   __syncthreads();
   // 16 lanes to a token issue the fewest instructions (64 tokens, 256 experts,
   // k 8: 9.3 us against 13.4 with 64 lanes), 64 lanes have the shorter chain
@@ -194,6 +200,14 @@ __device__ __forceinline__ int rank_in(const uint32_t* bits, int E, int e, int i
   return i >> 5 ? r + __builtin_popcount(bits[e]) : r;
 }
 
+// Tokens of the block that chose expert e.
+template <int WORDS>
+__device__ __forceinline__ int chose(const uint32_t* bits, int E, int e) {
+  int c = __builtin_popcount(bits[e]);
+  if constexpr (WORDS == 2) c += __builtin_popcount(bits[E + e]);
+  return c;
+}
+
 // Exclusive prefix of v[0 .. E) in place by the first wave, v[E] = the total.
 __device__ __forceinline__ void scan_experts(int32_t* v, int E) {
   if (threadIdx.x < 64) {
@@ -217,7 +231,7 @@ __global__ __launch_bounds__(1024) void route_one_kernel(RouteArgs a) {
   const int tid = threadIdx.x;
   choose_block<16>(a, 0, a.T, bits);
   for (int e = tid; e < a.E; e += 1024) {
-    first[e] = __builtin_popcount(bits[e]) + __builtin_popcount(bits[a.E + e]);
+    first[e] = chose<2>(bits, a.E, e);
   }
   __syncthreads();
   scan_experts(first, a.E);
@@ -237,17 +251,18 @@ __global__ __launch_bounds__(1024) void route_one_kernel(RouteArgs a) {
   }
 }
 
-// Blocks of 64 tokens: choose, count, and leave each slot's rank inside the
-// block in pos.
-__global__ __launch_bounds__(1024) void route_choose_kernel(RouteArgs a) {
-  extern __shared__ uint32_t lds[];   // bits [2][E]
-  const int t0 = static_cast<int>(blockIdx.x) * kBlockTokens;
-  const int n = min(kBlockTokens, a.T - t0);
-  choose_block<16>(a, t0, n, lds);
+// Blocks of 4 WAVES tokens: choose, count, and leave each slot's rank inside
+// the block in pos.
+template <int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void route_choose_kernel(RouteArgs a) {
+  extern __shared__ uint32_t lds[];   // bits [WAVES / 8][E]
+  const int t0 = static_cast<int>(blockIdx.x) * 4 * WAVES;
+  const int n = min(4 * WAVES, a.T - t0);
+  choose_block<WAVES>(a, t0, n, lds);
   const int tid = threadIdx.x;
-  for (int e = tid; e < a.E; e += 1024)
-    a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = __builtin_popcount(lds[e]) + __builtin_popcount(lds[a.E + e]);
-  for (int i = tid; i < n * a.k; i += 1024) {
+  for (int e = tid; e < a.E; e += 64 * WAVES)
+    a.counts[static_cast<int64_t>(blockIdx.x) * a.E + e] = chose<WAVES / 8>(lds, a.E, e);
+  for (int i = tid; i < n * a.k; i += 64 * WAVES) {
     const int64_t at = static_cast<int64_t>(t0) * a.k + i;
     const int id = a.ids[at];
     a.pos[at] = id >= 0 ? rank_in(lds, a.E, id, i / a.k) : -1;
@@ -304,8 +319,8 @@ __global__ __launch_bounds__(1024) void route_place_kernel(RouteArgs a) {
   scan_experts(first, a.E);
   if (blk == 0)
     for (int e = tid; e <= a.E; e += 1024) a.slots[e] = first[e];
-  const int t0 = blk * kBlockTokens;
-  const int n = min(kBlockTokens, a.T - t0) * a.k, live = first[a.E];
+  const int t0 = blk * a.per;
+  const int n = min(a.per, a.T - t0) * a.k, live = first[a.E];
   for (int i = tid; i < n; i += 1024) {
     const int64_t at = static_cast<int64_t>(t0) * a.k + i;
     const int id = a.ids[at];
@@ -433,7 +448,7 @@ usw_status check_route(int32_t T, int32_t E, int32_t k) {
 
 size_t route_bytes(int32_t T, int32_t E) {
   if (T <= kOneTokens) return 0;
-  const int64_t blocks = (static_cast<int64_t>(T) + kBlockTokens - 1) / kBlockTokens;
+  const int64_t blocks = (static_cast<int64_t>(T) + block_tokens(T) - 1) / block_tokens(T);
   return static_cast<size_t>(4) * (blocks + 1) * E;
 }
 
@@ -484,8 +499,10 @@ usw_status usw_expert_route(const void* logits, int32_t l_type, int64_t ld, int3
   if (T <= kOneTokens) {
     route_one_kernel<<<1, 1024, (3 * E + 1) * sizeof(uint32_t), s>>>(a);
   } else {
-    a.blocks = (T + kBlockTokens - 1) / kBlockTokens;
-    route_choose_kernel<<<a.blocks, 1024, 2 * E * sizeof(uint32_t), s>>>(a);
+    a.per = block_tokens(T);
+    a.blocks = static_cast<int>((static_cast<int64_t>(T) + a.per - 1) / a.per);
+    if (a.per == 32) route_choose_kernel<8><<<a.blocks, 512, E * sizeof(uint32_t), s>>>(a);
+    else route_choose_kernel<16><<<a.blocks, 1024, 2 * E * sizeof(uint32_t), s>>>(a);
     const size_t lds = (2 * E + 1) * sizeof(uint32_t);
     while ((1 << a.lg_e) < E) ++a.lg_e;
     if (a.blocks > kAddBlocks) {
