@@ -217,10 +217,18 @@ ExpertPlan plan_expert(const usw_expert_fmt* f, const usw::Geometry& g, int32_t 
   p.tiles = active + (S - active) / chunk;
   p.ring = p.lean && chunk == 16;
   // One round of resident workgroups over the tiles, as the plain product
-  // splits a matrix with that many strips.
+  // splits a matrix with that many strips.  Where it takes a workgroup per
+  // compute unit, half as many more: runs fill about two thirds of the tiles
+  // that p.tiles bounds (26 experts of 256x12288 with 38 rows each 66.7 us
+  // with 256 workgroups, 44.0 with 384; 8 of 1024x8192 with 38 rows 47.9 /
+  // 39.3; 512 or more no better there, 4 of 512x16384 with 50 rows 33.0 / 27.4
+  // / 32.2 with 512).
   usw::Geometry gt = g;
   gt.Gr = g.Gr * p.tiles;
-  const Plan one = make_plan<ExpertArgs>(gt, chunk, 0, i4, p.lean);
+  int64_t want = 0;
+  if (chunk == 64 && gt.Gr <= kComputeUnits)
+    want = std::min<int64_t>(kComputeUnits * 3 / 2 / gt.Gr, std::max<int64_t>(1, g.Gc / 12));
+  const Plan one = make_plan<ExpertArgs>(gt, chunk, static_cast<int>(want), i4, p.lean);
   p.splits = one.splits;
   if (p.splits > 1) {
     p.cb = usw::counter_zone(static_cast<size_t>(4) * p.tiles * g.Gr);
