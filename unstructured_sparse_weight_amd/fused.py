@@ -339,14 +339,16 @@ def expert_route(logits, k: int, renormalize: bool = True, stream=None) -> Route
         if (one != 1 and E > 1) or (ld < E and T > 1):
             lg, ld = lg.contiguous(), E
         n = T * k
-        # The scratch counts go behind the plan's arrays: one allocation.
-        ids, pos, rows, offsets, rest = torch.empty(3 * n + E + 1 + need // 4, dtype=torch.int32, device=dev).split(
-            (n, n, n, E + 1, need // 4))
+        # One allocation: ids, pos, rows, offsets, and behind them the scratch counts.
+        buf = torch.empty(3 * n + E + 1 + need // 4, dtype=torch.int32, device=dev)
         weights = torch.empty((T, k), dtype=torch.float32, device=dev)
-        check(lib().usw_expert_route(lg.data_ptr(), lt, ld if T > 1 else 0, T, E, k, renormalize, ids.data_ptr(),
-                                     weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(), pos.data_ptr(),
-                                     rest.data_ptr() if need else None, need, handle), "usw_expert_route")
-        return RoutePlan(ids.view(T, k), weights, offsets, rows, pos.view(T, k))
+        at, step = buf.data_ptr(), 4 * n
+        check(lib().usw_expert_route(lg.data_ptr(), lt, ld if T > 1 else 0, T, E, k, renormalize, at,
+                                     weights.data_ptr(), at + 3 * step, at + 2 * step, at + step,
+                                     at + 3 * step + 4 * (E + 1) if need else None, need, handle), "usw_expert_route")
+        two, by = (T, k), (k, 1)
+        return RoutePlan(buf.as_strided(two, by), weights, buf.as_strided((E + 1,), (1,), 3 * n),
+                         buf.as_strided((n,), (1,), 2 * n), buf.as_strided(two, by, n))
 
     return _on(dev, stream, body)
 
