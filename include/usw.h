@@ -665,8 +665,8 @@ usw_status usw_spmm_fused_workspace(const usw_fmt* fmt, int32_t N, int32_t split
 /*
  * Y [N][M] as above, X [N][K] fp16.  As usw_spmm_ex otherwise (layouts,
  * alignment, splits, workspace, stream, determinism).  Few rows take the
- * decode kernels in passes of up to 64; from 65 rows (large fp16 weights: 129
- * or 193) the weight is expanded once to dense fp16 in the workspace (2 M K
+ * decode kernels in passes of up to 128; from 65 rows (weights of more than
+ * 2^22 elements 129, fp16 of more than 2^26 193) the weight is expanded once to dense fp16 in the workspace (2 M K
  * bytes) and multiplied there, unless splits > 0.  ep may be NULL: no
  * epilogue.  ep and the struct it points to are read during the call.  Y may
  * be the residual itself (same address, ld_res = M); it may overlap nothing

@@ -155,6 +155,39 @@ def test_split_factors(splits, val, N):
     near(y, want, bound, "splits")
 
 
+@pytest.mark.parametrize("val", ["f16", "i4"])
+@pytest.mark.parametrize("N", [65, 80, 81, 96, 97, 128, 129, 200, 300])
+def test_long_passes(val, N):
+    """One pass of more than 64 rows, equal passes of up to 128 and a shorter
+    last one; slots of both sizes and the path of GroupTiles that fit none."""
+    M, K = 128, 1344
+    for density, splits in ((0.4, 1), (0.65, 3), (0.97, 2), (0.5, 5)):
+        enc, Wd = weight(M, K, density, val, 95)
+        rng = np.random.default_rng(96 + N)
+        x, b, mul, res = half(rng, N, K), half(rng, M), half(rng, N, M), half(rng, N, M)
+        for out in ("f16", "f32"):
+            say(f"[fused] long pass N={N} {val} density {density} splits={splits} {out}")
+            y = usw.spmm_fused(enc, gpu(x), bias=gpu(b), act="gelu", mul=gpu(mul), residual=gpu(res),
+                               out_dtype=DT[out], splits=splits)
+            z = usw.spmm_fused(enc, gpu(x), bias=gpu(b), act="gelu", mul=gpu(mul), residual=gpu(res),
+                               out_dtype=DT[out], splits=splits)
+            assert torch.equal(y, z)
+            want, bound = ref.product(Wd, x, b, "gelu", mul, res, out, val == "i4")
+            near(y, want, bound, "long pass")
+
+
+@pytest.mark.parametrize("val", ["f16", "i4"])
+@pytest.mark.parametrize("N", [66, 90, 127])
+def test_long_passes_integer_exact(val, N):
+    M, K = 2112, 2048   # more than 2^22 elements: passes without a split factor asked for
+    enc, Wd = weight(M, K, 0.5, val, 97, exact=True)
+    x = wl.activations_small_int(N, K, np.random.default_rng(98))
+    say(f"[fused] long pass exact {val} N={N}")
+    y = usw.spmm_fused(enc, gpu(x), act="relu", out_dtype=torch.float32)
+    want, _ = ref.product(Wd, x, None, "relu", None, None, "f32")
+    assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
+
+
 # Every tiling of the expanded product: small tiles with and without splits,
 # medium ones with and without, large ones in whole rounds and with tiles left
 # over; outputs and rows that end inside a tile.  The references are of some

@@ -41,7 +41,8 @@ def exact(M, K, density, i4, seed):
 # The ring kernel, the per-wave kernel (more rows, denser, INT4), with splits;
 # expanded: small, medium and large tiles, columns that end a ring early.
 CASES = [(512, 1024, 8, 0.5, False, 3), (256, 512, 40, 0.5, False, 0), (256, 512, 9, 0.9, False, 0),
-         (256, 512, 9, 0.5, True, 2), (256, 512, 60, 0.5, True, 0), (192, 64, 70, 0.5, False, 0),
+         (256, 512, 9, 0.5, True, 2), (256, 512, 60, 0.5, True, 0), (256, 512, 77, 0.5, False, 1),
+         (256, 1088, 90, 0.9, False, 2), (256, 512, 120, 0.5, True, 1), (192, 64, 70, 0.5, False, 0),
          (192, 320, 200, 0.7, True, 0), (2624, 832, 2050, 0.5, False, 0), (4096, 768, 4096, 0.5, False, 0)]
 
 

@@ -199,22 +199,41 @@ __device__ __forceinline__ void finish_strip_fused(const A& a, int gi, int sidx,
                 static_cast<uint32_t>(a.splits - 1);
   __syncthreads();
   if (!last_flag) return;
-  for (int e = tid; e < 16 * a.N; e += nthreads) {
-    const int n = e >> 4;
-    const int ml = 4 * (e & 15);
-    const int off = (n * a.M + m0 + ml) * 4;
-    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-    for (int p0 = 0; p0 < a.splits; p0 += AHEAD) {
-      f32x4_t v[AHEAD];
+  // Every output of a thread at once (of eight token blocks, half), so that
+  // one round trip brings AHEAD splits of all of them (MI355X, 4096x11008 N =
+  // 77: the last workgroup takes 3.7 us one output after another, 1.9 together).
+  constexpr int kEach = NB == 8 ? 4 : NB;
+  for (int e0 = tid; e0 < 16 * a.N; e0 += kEach * nthreads) {
+    f32x4_t sum[kEach];
+    int off[kEach];
 #pragma unroll
-      for (int j = 0; j < AHEAD; ++j)
-        if (p0 + j < a.splits)
-          v[j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(part_rsrc(p0 + j), off, 0, kCacheSc1));
-#pragma unroll
-      for (int j = 0; j < AHEAD; ++j)
-        if (p0 + j < a.splits) sum += v[j];
+    for (int i = 0; i < kEach; ++i) {
+      const int e = e0 + i * nthreads;
+      sum[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      off[i] = e < 16 * a.N ? ((e >> 4) * a.M + m0 + 4 * (e & 15)) * 4 : 0x7FFFFFF0;   // past the bound: zeros
     }
-    store_y4(n, ml, sum);
+    for (int p0 = 0; p0 < a.splits; p0 += AHEAD) {
+      f32x4_t v[AHEAD][kEach];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j)
+        if (p0 + j < a.splits) {
+          const auto r = part_rsrc(p0 + j);
+#pragma unroll
+          for (int i = 0; i < kEach; ++i)
+            v[j][i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, off[i], 0, kCacheSc1));
+        }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j)
+        if (p0 + j < a.splits) {
+#pragma unroll
+          for (int i = 0; i < kEach; ++i) sum[i] += v[j][i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = e0 + i * nthreads;
+      if (e < 16 * a.N) store_y4(e >> 4, 4 * (e & 15), sum[i]);
+    }
   }
   if (tid == 0) __hip_atomic_store(&a.counters[gi], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -625,7 +644,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
     return sum;
   };
   if constexpr (ArgTraits<A>::kEpilogue)
-    finish_strip_fused<NB, I4, 8>(a, gi, sidx, kThreads, last_flag, sum_of);
+    finish_strip_fused<NB, I4, NB == 1 ? 8 : 4>(a, gi, sidx, kThreads, last_flag, sum_of);
   else
     finish_strip<NB, I4, OUT_F16>(a, gi, sidx, kThreads, last_flag, sum_of);
 }

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "usw.h"
 #include "usw_decode_kernels.h"
@@ -23,6 +24,15 @@ using DefaultCfgLean = Cfg<4, 1, 5>;
 using DefaultCfg2 = Cfg<4, 1, 3>;
 // 33..64 columns of N in one pass (four token blocks): two waves per SIMD.
 using DefaultCfg4 = Cfg<4, 1, 2>;
+// 65..128 columns in one pass (five, six or eight token blocks; only the fused
+// product: by expert there are tiles enough to fill the chip, and two smaller
+// ones beat one of 128 rows, 8 experts of 4096x4096 with 100 rows each 91.6
+// against 112.5 us): one wave per SIMD, whose 512 registers hold up to 128
+// accumulators and two GroupTiles' X fragments.  Two passes rebuild the
+// weight twice (MI355X, two passes / one: 4096x11008 N = 77 41.4 / 27.6 us,
+// 8192x8192 N = 128 60.8 / 46.4).  Not faster at N = 77: three slots 2.6% behind,
+// eight waves of half the columns equal there, spilling above 80 columns.
+using DefaultCfg8 = Cfg<4, 1, 1>;
 // INT4 values, up to 16 columns of N: a third of the fp16 slot registers
 // (85 VGPRs), so a fifth wave per SIMD fits and hides more of the rebuild
 // latency (measured 6% faster on the 20480x5120 layer at N = 2).
@@ -34,6 +44,7 @@ struct CfgInfo {
 };
 
 CfgInfo cfg_info(int nchunk, bool i4, bool lean) {
+  if (nchunk > 64) return CfgInfo{DefaultCfg8::kWavesPerGroup, DefaultCfg8::kOcc};
   if (nchunk > 32) return CfgInfo{DefaultCfg4::kWavesPerGroup, DefaultCfg4::kOcc};
   if (nchunk > 16) return CfgInfo{DefaultCfg2::kWavesPerGroup, DefaultCfg2::kOcc};
   if (i4) return CfgInfo{DefaultCfgI4::kWavesPerGroup, DefaultCfgI4::kOcc};
@@ -47,9 +58,9 @@ constexpr int64_t kComputeUnits = 256;
 
 struct Plan {
   int splits;     // workgroups per 64-row strip, passes of nchunk tokens
-  int nchunk;     // columns of N per kernel pass (16, 32 or 64)
-  int rsplits;    // the same for the last pass when it is shorter (N > 64,
-  int rchunk;     // N mod 64 tokens in a pass of rchunk), else splits, 0
+  int nchunk;     // columns of N per kernel pass (pass_chunk)
+  int rsplits;    // the same for the last pass when it is shorter (N mod
+  int rchunk;     // nchunk tokens in a pass of rchunk), else splits, 0
   int waves;      // waves per workgroup
   bool ring;      // the workgroup-cooperative kernel
 };
@@ -94,8 +105,20 @@ bool lean_values(const usw_fmt* f, const usw::Geometry& g) {
          static_cast<double>(f->nnz) <= 0.55 * static_cast<double>(g.M) * static_cast<double>(g.K);
 }
 
-// Pass size (16, 32 or 64 tokens) that n tokens take.
-int pass_chunk(int n) { return n <= 16 ? 16 : n <= 32 ? 32 : 64; }
+// Pass size that n tokens take: 16, 32 or 64 tokens or, where passes may be
+// as long, 80, 96 or 128.
+int pass_chunk(int n, int longest) {
+  const int c = n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : n <= 80 ? 80 : n <= 96 ? 96 : 128;
+  return std::min(c, longest);
+}
+
+// Longest pass: a pass's rows of partial sums are addressed in 32 bits.
+template <class A>
+constexpr bool kTallPasses = ArgTraits<A>::kEpilogue && !ArgTraits<A>::kExperts;
+template <class A>
+int longest_pass(const usw::Geometry& g) {
+  return kTallPasses<A> && g.M <= (int64_t(1) << 21) ? 128 : 64;
+}
 
 // Split factor of the per-wave decode kernel for passes of `chunk` tokens.
 int wave_splits(const usw::Geometry& g, int chunk, int splits_req, bool i4, bool lean) {
@@ -112,7 +135,7 @@ int wave_splits(const usw::Geometry& g, int chunk, int splits_req, bool i4, bool
     // 3; 4096x11008 27.3 with 4 against 31.0 with 8; 15360x5120 38.1 with 1
     // against 44.5 with 2).
     const int64_t target = kComputeUnits * 4 * ci.occ / ci.waves;
-    if (chunk == 64 && g.Gr <= kComputeUnits)
+    if (chunk >= 64 && g.Gr <= kComputeUnits)
       s = kComputeUnits / g.Gr;
     else
       s = std::max<int64_t>(1, (target + g.Gr / 2) / g.Gr);
@@ -128,7 +151,9 @@ int wave_splits(const usw::Geometry& g, int chunk, int splits_req, bool i4, bool
 template <class A = Args>
 Plan make_plan(const usw::Geometry& g, int N, int splits_req, bool i4, bool lean) {
   Plan p;
-  p.nchunk = pass_chunk(N);
+  // More tokens than the longest pass: equal passes.
+  const int longest = longest_pass<A>(g), passes = static_cast<int>((static_cast<int64_t>(N) + longest - 1) / longest);
+  p.nchunk = pass_chunk(longest > 64 ? (N - 1) / passes + 1 : N, longest);
   p.rchunk = 0;
   p.ring = !i4 && lean && N <= 16;
   if (p.ring) {
@@ -154,7 +179,7 @@ Plan make_plan(const usw::Geometry& g, int N, int splits_req, bool i4, bool lean
   p.splits = wave_splits(g, p.nchunk, splits_req, i4, lean);
   // A shorter last pass gets the split factor of its own size.
   const int rem = N > p.nchunk ? N % p.nchunk : 0;
-  p.rchunk = rem > 0 ? pass_chunk(rem) : 0;
+  p.rchunk = rem > 0 ? pass_chunk(rem, longest) : 0;
   p.rsplits = rem > 0 ? wave_splits(g, p.rchunk, splits_req, i4, lean) : p.splits;
   return p;
 }
@@ -199,7 +224,9 @@ void launch_cfg(const A& a, bool f16out, dim3 grid, hipStream_t s) {
 
 template <int NB, bool I4, int CH, class A>
 void launch_decode(const A& a, bool f16out, dim3 grid, hipStream_t s) {
-  if constexpr (NB == 4)
+  if constexpr (NB > 4)
+    launch_cfg<NB, I4, CH, DefaultCfg8>(a, f16out, grid, s);
+  else if constexpr (NB == 4)
     launch_cfg<NB, I4, CH, DefaultCfg4>(a, f16out, grid, s);
   else if constexpr (NB == 2)
     launch_cfg<NB, I4, CH, DefaultCfg2>(a, f16out, grid, s);
@@ -211,9 +238,20 @@ void launch_decode(const A& a, bool f16out, dim3 grid, hipStream_t s) {
     launch_cfg<NB, I4, CH, DefaultCfg>(a, f16out, grid, s);
 }
 
-// One pass of nb 16-token blocks (1, 2 or 4).
+// One pass of nb 16-token blocks (1, 2 or 4; the fused product 5, 6 or 8 too).
 template <class A>
 void launch_pass(const A& a, bool ring, bool i4, bool lean, int nb, bool f16out, dim3 grid, hipStream_t s) {
+  if constexpr (kTallPasses<A>) {
+    auto tall = [&](auto blocks) {
+      constexpr int NB = decltype(blocks)::value;
+      if (i4) launch_decode<NB, true, 3>(a, f16out, grid, s);
+      else if (lean) launch_decode<NB, false, 5>(a, f16out, grid, s);
+      else launch_decode<NB, false, 6>(a, f16out, grid, s);
+    };
+    if (nb == 5) return tall(std::integral_constant<int, 5>{});
+    if (nb == 6) return tall(std::integral_constant<int, 6>{});
+    if (nb == 8) return tall(std::integral_constant<int, 8>{});
+  }
   if (ring) {
     ring_launch(a, f16out, grid, s);
   } else if (i4) {

@@ -61,19 +61,19 @@ struct FusedPlan {
 
 bool fits_wide(const usw::Geometry& g) { return g.M <= kMaxLd; }
 
-// Rows from which the weight is expanded; fewer take passes of up to 64 rows
-// that rebuild it each time.  Two passes cost as much as the expansion and
-// the product on weights of about 2^24 elements and on all INT4 weights,
-// whose expansion reads less (MI355X, passes / expanded: 1152x1152 N = 80
-// 20.6 / 12.5 us, 4096x4096 N = 70 26.5 / 27.6 and N = 100 28.5 / 26.2, INT4
-// 20480x5120 N = 128 105 / 88); on larger ones three (11008x4096 N = 96 45.9
-// / 48.5, N = 128 51.9 / 50.1), on the largest four (20480x5120 N = 160 137 /
-// 148, N = 200 165 / 160).  A caller's split factor asks for the passes.
+// Rows from which the weight is expanded; fewer take passes of up to 128 rows
+// that rebuild it each time (MI355X, passes / expanded).  Weights of up to
+// 2^22 elements, whose expansion is short: 640x640 N = 96 11.8 / 9.9 us,
+// 2048x2048 N = 72 17.9 / 17.0, N = 128 24.0 / 17.4.  Above, one pass is ahead:
+// 4096x4096 N = 128 26.3 / 27.0, 11008x4096 N = 96 32.7 / 50.8, N = 128 41.4 /
+// 51.2; two are not, 4096x4096 N = 160 36.5 / 31.8, 11008x4096 N = 192 64.1 /
+// 59.8, except on the largest fp16 weights: 20480x5120 N = 160 130 / 149, N =
+// 192 149 / 170, N = 256 194 / 189; INT4, whose expansion reads less, N = 160
+// 136 / 132.  A caller's split factor asks for the passes.
 bool use_wide(const usw_fmt* f, const usw::Geometry& g, int32_t N, int splits_req) {
   const int64_t elements = g.M * g.K;
-  const int from = f->val_type == USW_VAL_I4 || elements <= (int64_t(1) << 24) ? 64
-                   : elements <= (int64_t(1) << 26)                            ? 128
-                                                                               : 192;
+  const bool largest = elements > (int64_t(1) << 26) && f->val_type == USW_VAL_F16;
+  const int from = elements <= (int64_t(1) << 22) ? 64 : largest ? 192 : 128;
   return N > from && splits_req <= 0 && fits_wide(g);
 }
 
@@ -158,7 +158,7 @@ usw_status fused_impl(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_ty
     a.e = e;
     if (e.mul) a.e.mul += e.ld_mul * n0;
     if (e.res) a.e.res += e.ld_res * n0;
-    const int nb = nc > 32 ? 4 : nc > 16 ? 2 : 1;
+    const int nb = pass_chunk(nc, p.nchunk) / 16;
     launch_pass(a, p.ring, i4, lean, nb, e.f16out, dim3(static_cast<unsigned>(nblk)), s);
     if (hipGetLastError() != hipSuccess) return USW_ERR_HIP;
   }
