@@ -127,7 +127,7 @@ int wave_splits(const usw::Geometry& g, int chunk, int splits_req, bool i4, bool
   if (s <= 0) {
     // About one round of resident workgroups (occ waves per SIMD, 4 SIMDs
     // per compute unit), each wave keeping at least 3 GroupTiles to stream.
-    // Passes of 64 tokens on a matrix with at most one strip per compute
+    // Passes of 64 tokens and more on a matrix with at most one strip per compute
     // unit take as many workgroups as there are compute units, no more: the
     // split partial sums (64 x M fp32 per split, written and read back) then
     // cost more than the second workgroup per compute unit gains (measured
