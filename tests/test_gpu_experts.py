@@ -137,7 +137,8 @@ def test_integer_exact_is_bitwise(val, density, counts):
 # and experts without rows (whose weights are not expanded).  The references
 # are of some rows of every run.
 EXPANDED = [([200, 0, 320, 131], 192, 320, "small"), ([500, 900, 0, 700], 1280, 1664, "medium"),
-            ([2100, 100, 1900, 0, 2300], 2112, 128, "small, many"), ([2100, 300, 1900, 0, 2300], 2560, 5120, "large")]
+            ([2100, 100, 1900, 0, 2300], 2112, 128, "small, many"), ([2100, 300, 1900, 0, 2300], 2560, 5120, "large"),
+            ([40, 35, 0, 90], 192, 64, "one column"), ([150, 90, 3, 100], 320, 256, "few columns")]
 
 
 @pytest.mark.parametrize("counts,M,K,what", EXPANDED, ids=[e[3] for e in EXPANDED])

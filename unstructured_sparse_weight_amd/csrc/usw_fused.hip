@@ -204,8 +204,13 @@ ExpertPlan plan_expert(const usw_expert_fmt* f, const usw::Geometry& g, int32_t 
   // up to 2^26 elements in all, where the passes leave compute units idle,
   // 128 (8 experts of 2048x2048: 43.9 us in passes, 42.9 expanded; 16 of
   // 2048x1024, 250 rows each: 69.8 / 50.9); above, 224 (8 of 11008x4096, 200
-  // rows each: 428 / 481; 8 of 4096x11008, 500 rows each: 800 / 684).
-  p.wide = mean >= (f->E * g.M * g.K <= (int64_t(1) << 26) ? 128 : 224) && fits_wide(g);
+  // rows each: 428 / 481; 8 of 4096x11008, 500 rows each: 800 / 684).  With up
+  // to 4 GroupTile columns, less than one for each wave of a split, 80 (26 of
+  // 8192x256, 88 rows each: 82.2 / 65.5; 8 of 8192x256, 64 rows: 25.4 / 27.8),
+  // with one column 32 (8 of 4096x64, 32 rows each: 10.2 / 10.4; 26 of
+  // 12672x64, 88 rows: 107 / 48.3).
+  const int from = g.Gc == 1 ? 32 : g.Gc <= 4 ? 80 : f->E * g.M * g.K <= (int64_t(1) << 26) ? 128 : 224;
+  p.wide = mean >= from && fits_wide(g);
   if (p.wide) {
     p.w = usw::wide_plan(g, f->E, S);
     p.need = p.w.need;
