@@ -13,7 +13,8 @@
 // plans.
 //
 // Choosing is bound by the instructions it issues: k rounds of a maximum over
-// the experts, the lowest expert that has it, and its removal.  Four tokens
+// the experts, the lowest expert that has it (fp16 logits: part of the
+// maximum), and its removal.  Four tokens
 // share a wave, 16 lanes (a DPP row) to a token, so that the moves across lanes
 // serve four tokens each.
 //
@@ -69,7 +70,16 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return v > -__builtin_inff() ? key : 0u;
 }
 
+// An fp16 logit's key ends in bits that are all alike, so its last ten hold
+// the expert instead, the lower expert above: such keys are all different, and
+// a maximum is the choice itself (64 tokens of 256 experts, k 8: 9.3 us, fp32
+// logits 11.1).
+constexpr uint32_t kExpertBits = 0x3FFu;
+static_assert(kMaxRouteExperts <= kExpertBits + 1);
+
+template <bool F16>
 __device__ __forceinline__ float key_value(uint32_t key) {
+  if constexpr (F16) key = (key & 0x80000000u) ? key & ~kExpertBits : key | kExpertBits;
   return __builtin_bit_cast(float, (key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
@@ -118,7 +128,7 @@ __device__ __forceinline__ float lanes_sum(float v) {
 
 // Chooses for the block's tokens [t0, t0 + n), L lanes to a token and PER
 // logits to a lane (expert c + L i), and sets their bits in bits.
-template <int WAVES, int L, int PER>
+template <bool F16, int WAVES, int L, int PER>
 __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n, uint32_t* bits) {
   const int c = threadIdx.x & (L - 1);
   for (int i = threadIdx.x / L; i - static_cast<int>(threadIdx.x & 63) / L < n; i += 64 * WAVES / L) {
@@ -127,13 +137,17 @@ __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n,
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int64_t at = row + min(c + L * q, a.E - 1);
-      v[q] = a.f16 ? static_cast<float>(static_cast<const _Float16*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
+      if constexpr (F16) v[q] = static_cast<float>(static_cast<const _Float16*>(a.logits)[at]);
+      else v[q] = static_cast<const float*>(a.logits)[at];
     }
     uint32_t key[PER], top = 0, mine = 0;
     float all = 0.0f;
     int id = -1;
 #pragma unroll
-    for (int q = 0; q < PER; ++q) key[q] = c + L * q < a.E ? order_key(v[q]) : 0u;
+    for (int q = 0; q < PER; ++q) {
+      key[q] = c + L * q < a.E ? order_key(v[q]) : 0u;
+      if (F16 && key[q]) key[q] = (key[q] | kExpertBits) - static_cast<uint32_t>(c + L * q);
+    }
     for (int j = 0; j < a.k; ++j) {
       uint32_t best = key[0];
 #pragma unroll
@@ -144,22 +158,29 @@ __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n,
         if (!a.renormalize) {
 #pragma unroll
           for (int q = 0; q < PER; ++q)
-            if (key[q]) all += exp_below(key_value(key[q]), key_value(top));
+            if (key[q]) all += exp_below(key_value<F16>(key[q]), key_value<F16>(top));
         }
       }
-      // The lowest expert that has it, as the largest complement.
-      uint32_t at = 0;
+      if constexpr (F16) {
+        mine = c == j ? best : mine;
 #pragma unroll
-      for (int q = PER - 1; q >= 0; --q) at = key[q] == best ? ~static_cast<uint32_t>(L * q) - c : at;
-      const int e = static_cast<int>(~lanes_max<L>(at));
-      if (c == j && best != 0) {
-        id = e;
-        mine = best;
+        for (int q = 0; q < PER; ++q) key[q] = key[q] == best ? 0u : key[q];
+      } else {
+        // The lowest expert that has it, as the largest complement.
+        uint32_t at = 0;
+#pragma unroll
+        for (int q = PER - 1; q >= 0; --q) at = key[q] == best ? ~static_cast<uint32_t>(L * q) - c : at;
+        const int e = static_cast<int>(~lanes_max<L>(at));
+        if (c == j && best != 0) {
+          id = e;
+          mine = best;
+        }
+#pragma unroll
+        for (int q = 0; q < PER; ++q) key[q] = e - c == L * q ? 0u : key[q];
       }
-#pragma unroll
-      for (int q = 0; q < PER; ++q) key[q] = e - c == L * q ? 0u : key[q];
     }
-    const float p = mine ? exp_below(key_value(mine), key_value(top)) : 0.0f;
+    if (F16 && mine) id = static_cast<int>(kExpertBits - (mine & kExpertBits));
+    const float p = mine ? exp_below(key_value<F16>(mine), key_value<F16>(top)) : 0.0f;
     const float total = lanes_sum<L>(a.renormalize ? p : all);
     if (i < n && c < a.k) {
       const int64_t at = static_cast<int64_t>(t0 + i) * a.k + c;
@@ -170,27 +191,33 @@ __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n,
   }
 }
 
+template <bool F16, int WAVES>
+__device__ __forceinline__ void choose_in(const RouteArgs& a, int t0, int n, uint32_t* bits) {
+  // 16 lanes to a token issue the fewest instructions (64 tokens, 256 experts,
+  // k 8: 9.3 us against 13.4 with 64 lanes), 64 lanes have the shorter chain
+  // where one token is all a wave has (1 token: 4.3 us against 5.9).  Above 512
+  // experts the two are equal at 64 tokens, and 64 lanes keep fewer registers.
+  if (a.E > 512) choose_tokens<F16, WAVES, 64, 16>(a, t0, n, bits);
+  else if (n <= WAVES && a.E > 64) {
+    if (a.E <= 128) choose_tokens<F16, WAVES, 64, 2>(a, t0, n, bits);
+    else if (a.E <= 256) choose_tokens<F16, WAVES, 64, 4>(a, t0, n, bits);
+    else choose_tokens<F16, WAVES, 64, 8>(a, t0, n, bits);
+  } else if (a.E <= 16) choose_tokens<F16, WAVES, 16, 1>(a, t0, n, bits);
+  else if (a.E <= 32) choose_tokens<F16, WAVES, 16, 2>(a, t0, n, bits);
+  else if (a.E <= 64) choose_tokens<F16, WAVES, 16, 4>(a, t0, n, bits);
+  else if (a.E <= 128) choose_tokens<F16, WAVES, 16, 8>(a, t0, n, bits);
+  else if (a.E <= 256) choose_tokens<F16, WAVES, 16, 16>(a, t0, n, bits);
+  else choose_tokens<F16, WAVES, 16, 32>(a, t0, n, bits);
+}
+
 // Chooses for the block's tokens [t0, t0 + n), n <= 4 WAVES, and leaves each
 // expert's bitmap of the tokens that chose it in bits[WAVES / 8][E].
 template <int WAVES>
 __device__ __forceinline__ void choose_block(const RouteArgs& a, int t0, int n, uint32_t* bits) {
   for (int i = threadIdx.x; i < WAVES / 8 * a.E; i += 64 * WAVES) bits[i] = 0u;
   __syncthreads();
-  // 16 lanes to a token issue the fewest instructions (64 tokens, 256 experts,
-  // k 8: 9.3 us against 13.4 with 64 lanes), 64 lanes have the shorter chain
-  // where one token is all a wave has (1 token: 4.3 us against 5.9).  Above 512
-  // experts the two are equal at 64 tokens, and 64 lanes keep fewer registers.
-  if (a.E > 512) choose_tokens<WAVES, 64, 16>(a, t0, n, bits);
-  else if (n <= WAVES && a.E > 64) {
-    if (a.E <= 128) choose_tokens<WAVES, 64, 2>(a, t0, n, bits);
-    else if (a.E <= 256) choose_tokens<WAVES, 64, 4>(a, t0, n, bits);
-    else choose_tokens<WAVES, 64, 8>(a, t0, n, bits);
-  } else if (a.E <= 16) choose_tokens<WAVES, 16, 1>(a, t0, n, bits);
-  else if (a.E <= 32) choose_tokens<WAVES, 16, 2>(a, t0, n, bits);
-  else if (a.E <= 64) choose_tokens<WAVES, 16, 4>(a, t0, n, bits);
-  else if (a.E <= 128) choose_tokens<WAVES, 16, 8>(a, t0, n, bits);
-  else if (a.E <= 256) choose_tokens<WAVES, 16, 16>(a, t0, n, bits);
-  else choose_tokens<WAVES, 16, 32>(a, t0, n, bits);
+  if (a.f16) choose_in<true, WAVES>(a, t0, n, bits);
+  else choose_in<false, WAVES>(a, t0, n, bits);
   __syncthreads();
 }
 
