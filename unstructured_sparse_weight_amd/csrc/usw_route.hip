@@ -14,9 +14,8 @@
 //
 // Choosing is bound by the instructions it issues: k rounds of a maximum over
 // the experts, the lowest expert that has it (fp16 logits: part of the
-// maximum), and its removal.  Four tokens
-// share a wave, 16 lanes (a DPP row) to a token, so that the moves across lanes
-// serve four tokens each.
+// maximum), and its removal.  Four tokens share a wave, 16 lanes (a DPP row)
+// to a token, so that the moves across lanes serve four tokens each.
 //
 // Up to 64 tokens one workgroup does all of it in one launch, since there
 // the launches are the time (64 experts, k 8, 64 tokens: 5.0 us, a second
@@ -77,9 +76,9 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 constexpr uint32_t kExpertBits = 0x3FFu;
 static_assert(kMaxRouteExperts <= kExpertBits + 1);
 
-template <bool F16>
+template <bool UNIQUE>
 __device__ __forceinline__ float key_value(uint32_t key) {
-  if constexpr (F16) key = (key & 0x80000000u) ? key & ~kExpertBits : key | kExpertBits;
+  if constexpr (UNIQUE) key = (key & 0x80000000u) ? key & ~kExpertBits : key | kExpertBits;
   return __builtin_bit_cast(float, (key & 0x80000000u) ? (key & 0x7FFFFFFFu) : ~key);
 }
 
@@ -130,9 +129,13 @@ __device__ __forceinline__ float lanes_sum(float v) {
 // logits to a lane (expert c + L i), and sets their bits in bits.
 template <bool F16, int WAVES, int L, int PER>
 __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n, uint32_t* bits) {
+  constexpr bool kUnique = F16 && PER < 32;   // keys that hold the expert (with 32 a register would spill)
   const int c = threadIdx.x & (L - 1);
   for (int i = threadIdx.x / L; i - static_cast<int>(threadIdx.x & 63) / L < n; i += 64 * WAVES / L) {
     const int64_t row = (t0 + min(i, n - 1)) * a.ld;
+    uint32_t key[PER], top = 0, mine = 0;
+    float all = 0.0f;
+    int id = -1;
     float v[PER];
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
@@ -140,13 +143,10 @@ __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n,
       if constexpr (F16) v[q] = static_cast<float>(static_cast<const _Float16*>(a.logits)[at]);
       else v[q] = static_cast<const float*>(a.logits)[at];
     }
-    uint32_t key[PER], top = 0, mine = 0;
-    float all = 0.0f;
-    int id = -1;
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       key[q] = c + L * q < a.E ? order_key(v[q]) : 0u;
-      if (F16 && key[q]) key[q] = (key[q] | kExpertBits) - static_cast<uint32_t>(c + L * q);
+      if (kUnique && key[q]) key[q] = (key[q] | kExpertBits) - static_cast<uint32_t>(c + L * q);
     }
     for (int j = 0; j < a.k; ++j) {
       uint32_t best = key[0];
@@ -158,10 +158,10 @@ __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n,
         if (!a.renormalize) {
 #pragma unroll
           for (int q = 0; q < PER; ++q)
-            if (key[q]) all += exp_below(key_value<F16>(key[q]), key_value<F16>(top));
+            if (key[q]) all += exp_below(key_value<kUnique>(key[q]), key_value<kUnique>(top));
         }
       }
-      if constexpr (F16) {
+      if constexpr (kUnique) {
         mine = c == j ? best : mine;
 #pragma unroll
         for (int q = 0; q < PER; ++q) key[q] = key[q] == best ? 0u : key[q];
@@ -179,8 +179,8 @@ __device__ __forceinline__ void choose_tokens(const RouteArgs& a, int t0, int n,
         for (int q = 0; q < PER; ++q) key[q] = e - c == L * q ? 0u : key[q];
       }
     }
-    if (F16 && mine) id = static_cast<int>(kExpertBits - (mine & kExpertBits));
-    const float p = mine ? exp_below(key_value<F16>(mine), key_value<F16>(top)) : 0.0f;
+    if (kUnique && mine) id = static_cast<int>(kExpertBits - (mine & kExpertBits));
+    const float p = mine ? exp_below(key_value<kUnique>(mine), key_value<kUnique>(top)) : 0.0f;
     const float total = lanes_sum<L>(a.renormalize ? p : all);
     if (i < n && c < a.k) {
       const int64_t at = static_cast<int64_t>(t0 + i) * a.k + c;
@@ -198,11 +198,10 @@ __device__ __forceinline__ void choose_in(const RouteArgs& a, int t0, int n, uin
   // where one token is all a wave has (1 token: 4.3 us against 5.9).  Above 512
   // experts the two are equal at 64 tokens, and 64 lanes keep fewer registers.
   if (a.E > 512) choose_tokens<F16, WAVES, 64, 16>(a, t0, n, bits);
-  else if (n <= WAVES && a.E > 64) {
-    if (a.E <= 128) choose_tokens<F16, WAVES, 64, 2>(a, t0, n, bits);
-    else if (a.E <= 256) choose_tokens<F16, WAVES, 64, 4>(a, t0, n, bits);
-    else choose_tokens<F16, WAVES, 64, 8>(a, t0, n, bits);
-  } else if (a.E <= 16) choose_tokens<F16, WAVES, 16, 1>(a, t0, n, bits);
+  else if (n <= WAVES && a.E > 256) choose_tokens<F16, WAVES, 64, 8>(a, t0, n, bits);
+  else if (n <= WAVES && a.E > 128) choose_tokens<F16, WAVES, 64, 4>(a, t0, n, bits);
+  else if (n <= WAVES && a.E > 64) choose_tokens<F16, WAVES, 64, 2>(a, t0, n, bits);
+  else if (a.E <= 16) choose_tokens<F16, WAVES, 16, 1>(a, t0, n, bits);
   else if (a.E <= 32) choose_tokens<F16, WAVES, 16, 2>(a, t0, n, bits);
   else if (a.E <= 64) choose_tokens<F16, WAVES, 16, 4>(a, t0, n, bits);
   else if (a.E <= 128) choose_tokens<F16, WAVES, 16, 8>(a, t0, n, bits);
