@@ -251,7 +251,8 @@ def test_captured_calls_keep_their_own_workspaces():
     """Two graphs captured on one stream, replayed several times with eager
     calls and new inputs between: each replay equals the eager result."""
     say("[fused] graphs")
-    cases = [(256, 2560, 8, "f16"), (128, 1024, 100, "i4"), (192, 1280, 300, "f16")]
+    cases = [(256, 2560, 8, "f16"), (128, 1024, 100, "i4"), (192, 1280, 300, "f16"), (2112, 2048, 77, "f16"),
+             (2112, 2048, 120, "i4")]
     made = []
     for i, (M, K, N, val) in enumerate(cases):
         enc, Wd = weight(M, K, 0.5, val, 200 + i)
