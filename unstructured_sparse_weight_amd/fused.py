@@ -127,6 +127,7 @@ def _on(device, stream, body):
 
 
 _WS = {}   # (device index, raw stream) -> [workspace, its leading bytes that are zero between calls]
+_KEPT = 1 << 16   # leading bytes that a call without counters leaves alone
 # Held from taking a workspace until the call is enqueued: two threads on one
 # stream share it, and a call's launches must stay together.
 _LOCK = threading.Lock()
@@ -147,10 +148,12 @@ def _workspace(device, handle, nbytes, counter_bytes):
     ent = _WS.get((device.index, handle))
     if ent is None or ent[0].numel() < nbytes:
         ent = _WS[(device.index, handle)] = [torch.empty(nbytes, dtype=torch.uint8, device=device), 0]
-    if counter_bytes:      # none, or 64 KiB and more; calls without leave those alone
-        if ent[1] < counter_bytes:
-            ent[0][:counter_bytes].zero_()
-        ent[1] = counter_bytes
+    # Counters are none, or 64 KiB and more.  Behind its own a call writes sums
+    # or weights, and one without counters does so from 64 KiB on, so no more
+    # than that is still zero after it.
+    if ent[1] < counter_bytes:
+        ent[0][:counter_bytes].zero_()
+    ent[1] = counter_bytes or min(ent[1], _KEPT)
     return ent[0]
 
 
