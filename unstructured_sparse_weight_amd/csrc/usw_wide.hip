@@ -91,7 +91,7 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(ExpandArgs a)
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int e = a.e0 + static_cast<int>(blockIdx.y);
-  if (a.slots && min(a.slots[e + 1], a.S) <= max(a.slots[e], 0)) return;   // no rows read this weight
+  if (a.slots && min(a.slots[e + 1], a.S) <= max(a.slots[e], 0)) return;   // no rows read this weight (scan_runs)
   if constexpr (I4) {
     for (int i = tid; i < 256; i += 64 * kExpandWaves) reinterpret_cast<u32x2_t*>(lut)[i] = row_byte_selectors(i);
   } else if (tid < 16) {
@@ -181,26 +181,34 @@ struct WideTile {
   int e, strip0, row0, n;
 };
 
-__device__ __forceinline__ void run_of(const WideArgs& a, int e, int* lo, int* hi) {
-  if (!a.slots) {
-    *lo = 0;
-    *hi = a.S;
-    return;
-  }
-  *lo = min(max(a.slots[e], 0), a.S);
-  *hi = min(max(a.slots[e + 1], *lo), a.S);
+// Inclusive maximum over the lanes up to this one (wave_inclusive_scan's steps).
+__device__ __forceinline__ int wave_inclusive_max(int v) {
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false));   // row_shr:1, 2, 4, 8
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false));
+  v = max(v, __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false));   // row_bcast:15, 31
+  return max(v, __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false));
 }
 
 // Scans the runs of the group's experts, 64 at a time: found(first expert,
 // tiles before, this lane's tiles of rows, inclusive tiles up to this lane, its
 // run) until it returns true.  Returns the tiles seen.
+//
+// An offset below one before it counts as that one, so whatever the array
+// holds the runs are disjoint parts of [0, S) and make no more tiles than the
+// host planned counters and partial sums for.
 template <int BN, class Fn>
 __device__ __forceinline__ int scan_runs(const WideArgs& a, int lane, Fn found) {
-  int before = 0;
+  int before = 0, top = 0;
   for (int b = a.e0; b < a.e1; b += 64) {
     const int e = min(b + lane, a.e1 - 1);
-    int lo, hi;
-    run_of(a, e, &lo, &hi);
+    int lo = 0, hi = a.S;
+    if (a.slots) {
+      lo = max(top, wave_inclusive_max(min(max(a.slots[e], 0), a.S)));
+      hi = max(lo, min(a.slots[e + 1], a.S));
+      top = __builtin_amdgcn_readlane(hi, 63);
+    }
     if (b + lane >= a.e1) hi = lo;
     const uint32_t nt = static_cast<uint32_t>(hi - lo + BN - 1) / BN;
     const uint32_t incl = wave_inclusive_scan(nt * a.mt);
