@@ -389,20 +389,36 @@ __device__ __forceinline__ uint32_t bitmap_prefix_reg(u32x2_t bm) {
   return wave_inclusive_scan(pc) - pc;
 }
 
+// How a product of INT4 codes loses the offset that its expanded rows carry
+// (code_offset_collect).  The plain product collects the offset's share of the
+// sums and takes it out at the end: its sums then round at the scale of
+// 72 sum|x| over all of a wave's columns, which grows with them where x is all
+// positive, as a ReLU leaves it (512x20480 in one split, 100 rows: 4.6e-4 of
+// the output off, an fp16 output's own rounding 2.1e-4; fp32 outputs 4e-6 with
+// x of both signs).  The products with an epilogue keep the sums at the scale
+// of the codes:
+//   kEach: four packed subtractions take it out of every slot, exactly (INT4
+//     5120x20480 N = 64: 44.9 us collected, 39.8 so; N = 128: 71.4 / 68.1;
+//     N = 24: 30.8 / 30.4; the subtractions serve all token blocks).
+//   kStep: one token block with fp16 output, where the subtractions would cost
+//     2 to 6% and the matrix cores idle: a product with the offset's negative
+//     goes into the same accumulator before each step's own, so no more than
+//     72 sum|x| of one step of 32 columns is ever in it (20480x5120 N = 8:
+//     19.3 us collected, 19.8 so, 20.4 by subtractions; 11008x4096 N = 16:
+//     15.7 / 15.9 / 16.4).
+enum class CodeOffset { kCollect, kEach, kStep };
+
 // Rebuild and multiply fragments f = F0 .. F1-1 (both ks) of a GroupTile
 // whose bitmap table is at tab and whose values are in the LDS staging area
 // starting at vals.  INT4 rows carry the expansion's offset: corr collects
-// its correction (code_offset_collect, all four fragments of a GroupTile at once).
-// EXACT takes the offset out of every slot instead, four packed subtractions a
-// row: the sums then round at the scale of the product and not of 72 sum|x|,
-// which an fp32 output shows (relative error 2e-7 against 4e-6) and an fp16
-// one, 2e-4 off anyway, does not; it costs 6 to 15% of the pass.
-template <int NB, bool I4, int F0 = 0, int F1 = 4, bool EXACT = false>
+// its correction (code_offset_collect, all four fragments of a GroupTile at
+// once) unless OFFSET takes it out here.
+template <int NB, bool I4, int F0 = 0, int F1 = 4, CodeOffset OFFSET = CodeOffset::kCollect>
 __device__ __forceinline__ void tile_mma(const u32x4_t (&x)[2][NB], const uint8_t* vals, const uint8_t* tab,
                                          const uint32_t* lut, f32x4_t (&acc)[4][NB], f32x4_t (&corr)[NB],
                                          const LaneMap& lm) {
   static_assert(!I4 || (F0 == 0 && F1 == 4), "the INT4 correction covers whole GroupTiles");
-  if constexpr (I4 && !EXACT) code_offset_collect<NB>(corr, x);
+  if constexpr (I4 && OFFSET == CodeOffset::kCollect) code_offset_collect<NB>(corr, x);
   u32x2_t e[F1 - F0][2];
 #pragma unroll
   for (int f = F0; f < F1; ++f)
@@ -416,7 +432,15 @@ __device__ __forceinline__ void tile_mma(const u32x4_t (&x)[2][NB], const uint8_
       const uint32_t word = e[f - F0][ks].x;
       const uint32_t rb = e[f - F0][ks].y + __builtin_popcount(word & lm.pmask);
       half8_t a = rebuild_row<I4>(vals, lut, rb, __builtin_amdgcn_ubfe(word, lm.sh, 8));
-      if constexpr (I4 && EXACT) a -= static_cast<_Float16>(kCodeOffset);
+      if constexpr (I4 && OFFSET == CodeOffset::kEach) a -= static_cast<_Float16>(kCodeOffset);
+      if constexpr (I4 && OFFSET == CodeOffset::kStep) {
+        const _Float16 m = static_cast<_Float16>(-kCodeOffset);
+        const half8_t neg = {m, m, m, m, m, m, m, m};
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          acc[f][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(neg, __builtin_bit_cast(half8_t, x[ks][nb]), acc[f][nb],
+                                                              0, 0, 0);
+      }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
         acc[f][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, __builtin_bit_cast(half8_t, x[ks][nb]), acc[f][nb], 0,
@@ -441,7 +465,10 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
   constexpr int kW = C::kWavesPerGroup;
   constexpr int kThreads = C::kThreadsPerGroup;
   constexpr int kD = C::kDepth;
-  constexpr bool kExact = ArgTraits<A>::kEpilogue && !OUT_F16;   // INT4 with fp32 output
+  constexpr CodeOffset kOffset = !ArgTraits<A>::kEpilogue ? CodeOffset::kCollect
+                                 : OUT_F16 && NB == 1     ? CodeOffset::kStep
+                                                          : CodeOffset::kEach;
+  constexpr bool kCollected = I4 && kOffset == CodeOffset::kCollect;
   // Row selectors: fp16 16 nibble entries of two dwords, INT4 256 byte
   // entries of two dwords.
   __shared__ __attribute__((aligned(16))) uint32_t lut[I4 ? 512 : 32];
@@ -574,7 +601,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
       const int cn = min(c + 1, c_last);
       slot_load(s0, a, gi, cn, lane, off_at(cn), off_at(cn + 1), xrow);
       wave_sync();
-      tile_mma<NB, I4, 0, 4, kExact>(xc, smem, tab, lut, acc, corr, lm);
+      tile_mma<NB, I4, 0, 4, kOffset>(xc, smem, tab, lut, acc, corr, lm);
       wave_sync();
       write_tab(s0);
     }
@@ -605,7 +632,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
       __builtin_amdgcn_s_setprio(0);
       slot_commit(cur, vb, lane);
       wave_sync();
-      tile_mma<NB, I4, 0, 4, kExact>(cur.x, smem, tab, lut, acc, corr, lm);
+      tile_mma<NB, I4, 0, 4, kOffset>(cur.x, smem, tab, lut, acc, corr, lm);
       wave_sync();
       write_tab(after);
     };
@@ -620,7 +647,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
   }
 
   // Workgroup reduction over waves (fixed order).
-  if constexpr (I4 && !kExact) code_offset_finish<NB>(corr);
+  if constexpr (kCollected) code_offset_finish<NB>(corr);
   __syncthreads();
   float* red = reinterpret_cast<float*>(smem);   // [waves][4][NB][64 lanes][4]
 #pragma unroll
@@ -628,7 +655,7 @@ __global__ __launch_bounds__(C::kThreadsPerGroup, C::kOcc) void decode_kernel(A 
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
       *reinterpret_cast<f32x4_t*>(red + (((w * 4 + f) * NB + nb) * 64 + lane) * 4) =
-          I4 && !kExact ? acc[f][nb] + corr[nb] : acc[f][nb];
+          kCollected ? acc[f][nb] + corr[nb] : acc[f][nb];
   __syncthreads();
 
   auto sum_of = [&](int n, int ml) {

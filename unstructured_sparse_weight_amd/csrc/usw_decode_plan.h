@@ -213,7 +213,7 @@ size_t workspace_bytes(const usw::Geometry& g, const Plan& p) {
 
 template <int NB, bool I4, int CH, class C, class A>
 void launch_cfg(const A& a, bool f16out, dim3 grid, hipStream_t s) {
-  if constexpr (!ArgTraits<A>::kEpilogue || I4) {
+  if constexpr (!ArgTraits<A>::kEpilogue || (I4 && NB == 1)) {
     if (!f16out) {
       decode_kernel<NB, I4, CH, false, C, A><<<grid, C::kThreadsPerGroup, 0, s>>>(a);
       return;
