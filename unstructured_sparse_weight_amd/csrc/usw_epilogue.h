@@ -29,15 +29,17 @@ struct Epilogue {
 typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
 
 // GELU by erfc, which keeps its relative accuracy where v is negative; 1 + erf
-// would cancel there (v = -5: 4% off); it is the dearer of the two (11008x4096
-// N = 2048 242 us against 232, few rows equal).  GELU's tanh form is v times the logistic function of 2z, z = sqrt(2/pi)
+// would cancel there (v = -5: 4% off).  It is the dearer of the two
+// (11008x4096 N = 2048 242 us against 232, few rows equal).
+//
+// GELU's tanh form is v times the logistic function of 2z, z = sqrt(2/pi)
 // (v + 0.044715 v^3), because (1 + tanh z) / 2 = 1 / (1 + exp(-2z)).  For
 // very negative v the exponential overflows to infinity and the product is
 // the limit, -0.  ReLU keeps NaN.  __expf is off by its argument's rounding,
-// z 2^-24 relative, which only shows where the output is e^z small.  The hardware's reciprocal is within one
-// unit in the last place, where an IEEE quotient would take ten instructions
-// more for each output (11008x4096 N = 2048, SiLU and mul: 220.6 us, with the
-// quotient 226.8).
+// z 2^-24 relative, which only shows where the output is a small e^z.  The
+// hardware's reciprocal is within one unit in the last place, where an IEEE
+// quotient would take ten instructions more for each output (11008x4096
+// N = 2048, SiLU and mul: 220.6 us, with the quotient 226.8).
 template <int ACT>
 __device__ __forceinline__ float activation(float v) {
   if constexpr (ACT == USW_ACT_RELU) return v < 0.0f ? 0.0f : v;
