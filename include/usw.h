@@ -672,7 +672,7 @@ usw_status usw_spmm_fused_workspace(const usw_fmt* fmt, int32_t N, int32_t split
  * be the residual itself (same address, ld_res = M); it may overlap nothing
  * else that the call reads.
  * Errors: as usw_spmm_ex, and BAD_DTYPE (act), BAD_SHAPE (a stride below M or
- * above 2^20, reserved), MISALIGNED (scales, bias, mul or res not 16-byte
+ * above 2^20, with more outputs than that 2^22, reserved), MISALIGNED (scales, bias, mul or res not 16-byte
  * aligned, a stride that is no multiple of 8), UNSUPPORTED (M > 2^22).
  */
 usw_status usw_spmm_fused(const usw_fmt* fmt, const uint16_t* X, void* Y, int32_t y_type, int32_t N,

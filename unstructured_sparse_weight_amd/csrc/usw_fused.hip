@@ -23,10 +23,12 @@ namespace {
 using namespace usw_dev;
 
 constexpr int kMaxExperts = 1024;
-// Longest stride of the epilogue's operands, and most outputs of an expanded
-// weight: the expanded product addresses a tile's rows with 32 bits.
+// Most outputs of an expanded weight, and longest stride of such a weight's
+// epilogue operands: the expanded product addresses a tile's rows with 32 bits.
 constexpr int64_t kMaxLd = int64_t(1) << 20;
 // Most outputs of a weight: a pass addresses its partial sums with 32 bits.
+// Also the longest stride where a weight has too many outputs to be expanded;
+// the passes address the operands with 64 bits.
 constexpr int64_t kMaxM = int64_t(1) << 22;
 
 // Checks an epilogue for rows of M outputs and fills the kernels' copy.
@@ -41,7 +43,8 @@ usw_status make_epilogue(const usw_epilogue* ep, int64_t M, int32_t y_type, Epil
   e->res = ep->res;
   if (ep->mul && ep->ld_mul != 0) e->ld_mul = ep->ld_mul;
   if (ep->res && ep->ld_res != 0) e->ld_res = ep->ld_res;
-  if (e->ld_mul < M || e->ld_res < M || (ep->mul && e->ld_mul > kMaxLd) || (ep->res && e->ld_res > kMaxLd))
+  const int64_t longest = M <= kMaxLd ? kMaxLd : kMaxM;
+  if (e->ld_mul < M || e->ld_res < M || (ep->mul && e->ld_mul > longest) || (ep->res && e->ld_res > longest))
     return USW_ERR_BAD_SHAPE;
   if (!aligned16(ep->bias) || !aligned16(ep->mul) || !aligned16(ep->res) || e->ld_mul % 8 || e->ld_res % 8)
     return USW_ERR_MISALIGNED;
@@ -106,10 +109,10 @@ usw_status fused_impl(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_ty
   if (!aligned16(X) || !aligned16(Y) || !aligned16(f->bitmaps) || !aligned16(f->values) ||
       (reinterpret_cast<uintptr_t>(f->offsets) & 3u) || (i4 && !aligned16(f->scales)))
     return USW_ERR_MISALIGNED;
+  if (g.M > kMaxM) return USW_ERR_UNSUPPORTED;
   Epilogue e;
   st = make_epilogue(ep, g.M, y_type, &e);
   if (st) return st;
-  if (g.M > kMaxM) return USW_ERR_UNSUPPORTED;
   const FusedPlan c = plan_fused(f, g, N, splits_req);
   if (c.need > 0) {
     if (!ws || ws_bytes < c.need) return USW_ERR_WORKSPACE;

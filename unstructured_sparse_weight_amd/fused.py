@@ -167,7 +167,7 @@ def _rows_operand(t, rows, M, device, what):
     ld, one = t.stride()
     if rows == 1:
         ld = M
-    if one != 1 or ld & 7 or ld < M or ld > 1 << 20 or t.data_ptr() & 15:
+    if one != 1 or ld & 7 or ld < M or ld > (1 << 20 if M <= 1 << 20 else 1 << 22) or t.data_ptr() & 15:
         t, ld = t.clone(memory_format=torch.contiguous_format), M
     return t, ld
 
