@@ -77,3 +77,27 @@ def test_sizes_in_turn():
         for j, (b, wb) in enumerate(cases):
             say(f"[sequence] {i} {j}")
             assert torch.equal(a(), wa) and torch.equal(b(), wb), (i, j)
+
+
+def test_released_workspaces():
+    """The memory goes back to torch's allocator, calls go on, a captured call
+    keeps its own."""
+    enc, W = integer_weight(4096, 4096, 0.5, 50)
+    x = integers(300, 4096, 51)
+    want = product(W, x)
+    say("[sequence] release")
+    fused.release_workspaces()
+    assert torch.equal(usw.spmm_fused(enc, x, out_dtype=torch.float32), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = usw.spmm_fused(enc, x, out_dtype=torch.float32)
+    held = torch.cuda.memory_allocated()
+    usw.release_workspaces()
+    assert held - torch.cuda.memory_allocated() >= 2 * 4096 * 4096
+    for _ in range(3):
+        y.zero_()
+        g.replay()
+        assert torch.equal(usw.spmm_fused(enc, x, out_dtype=torch.float32), want)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
+        usw.release_workspaces()

@@ -58,3 +58,14 @@ def test_the_library_asks_for_none_or_64_kib(M, K, val, N):
         need, cb = fused._expert_sizes(E, M, K, val, E * M * K // 2, E * M * K, N)
         assert cb == 0 or KEPT <= cb < need
         assert need == 0 or need > KEPT
+
+
+def test_release(workspace):
+    """Released workspaces are made again, their counters zero."""
+    call(workspace, 300000, 69632)
+    assert len(fused._WS) == 1
+    fused.release_workspaces()
+    assert not fused._WS
+    call(workspace, 200000, 69632)
+    fused.release_workspaces()
+    fused.release_workspaces()

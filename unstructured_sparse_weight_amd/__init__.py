@@ -22,7 +22,7 @@ import numpy as np
 from ._lib import (USW_OUT_F16, USW_OUT_F32, USW_VAL_F16, USW_VAL_I2, USW_VAL_I4, EXPORTED, UswCbcFmt, UswError,  # noqa: F401
                    UswFmt, UswUnionFmt, check, lib)
 from .fused import (ExpertBank, RoutePlan, expert_bank, expert_combine, expert_ffn, expert_route,  # noqa: F401
-                    expert_spmm, spmm_fused)
+                    expert_spmm, release_workspaces, spmm_fused)
 
 __all__ = ["HostEncoding", "Encoding", "encode_host", "encode", "to_device", "validate", "spmm",
            "spmm_workspace_bytes", "spmm_counter_bytes", "UnionHostEncoding", "UnionEncoding",
@@ -30,7 +30,7 @@ __all__ = ["HostEncoding", "Encoding", "encode_host", "encode", "to_device", "va
            "union_workspace_bytes", "CbcHostEncoding", "CbcEncoding", "cbc_encode_host", "cbc_encode",
            "cbc_to_device", "cbc_validate", "cbc_spmspv", "cbc_workspace_bytes", "save", "load", "UswError", "lib",
            "ExpertBank", "RoutePlan", "spmm_fused", "expert_bank", "expert_route", "expert_spmm", "expert_combine",
-           "expert_ffn"]
+           "expert_ffn", "release_workspaces"]
 
 _VAL = {"f16": USW_VAL_F16, "i4": USW_VAL_I4, "i2": USW_VAL_I2}
 

@@ -25,7 +25,7 @@ from ._lib import (USW_ACT, USW_OUT_F16, USW_OUT_F32, USW_VAL_I4, UswEpilogue, U
                    check, lib)
 
 __all__ = ["ExpertBank", "RoutePlan", "spmm_fused", "expert_bank", "expert_route", "expert_spmm", "expert_combine",
-           "expert_ffn"]
+           "expert_ffn", "release_workspaces"]
 
 
 @dataclass
@@ -155,6 +155,16 @@ def _workspace(device, handle, nbytes, counter_bytes):
         ent[0][:counter_bytes].zero_()
     ent[1] = counter_bytes or min(ent[1], _KEPT)
     return ent[0]
+
+
+def release_workspaces() -> None:
+    """Gives the workspaces that the fused and expert products keep, one per
+    stream they ran on, back to torch's allocator.  Each is as large as the
+    largest call on its stream asked for: 2 M K bytes where a weight was
+    expanded, up to 1 GiB and more.  The next call on a stream makes its own
+    again; graphs have theirs and are not touched."""
+    with _LOCK:
+        _WS.clear()
 
 
 def _rows_operand(t, rows, M, device, what):
