@@ -752,7 +752,7 @@ usw_status usw_expert_route(const void* logits, int32_t l_type, int64_t ld, int3
  *   res: fp16 [T][ld_res] or NULL (ld_res a multiple of 8, 0 = M); out may be
  *        res itself when out is fp16 and ld_res = M.
  *   out: [T][M] fp16 or fp32, 16-byte aligned.
- * Errors: NULL_ARG, BAD_N, BAD_SHAPE, BAD_DTYPE, MISALIGNED, UNSUPPORTED, HIP.
+ * Errors: NULL_ARG, BAD_N, BAD_SHAPE, BAD_DTYPE, MISALIGNED, HIP.
  */
 usw_status usw_expert_combine(const void* Y, int32_t y_type, int32_t S, int32_t M, const int32_t* pos,
                               const float* weights, int32_t T, int32_t k, const uint16_t* res, int64_t ld_res,

@@ -374,9 +374,11 @@ struct CombineArgs {
   const uint16_t* res;
   void* out;
   int64_t ld_res;
-  int64_t waves;   // T * parts
+  uint32_t waves;        // tokens of the launch * parts
   int S, M8, k, parts;   // parts: waves per token
 };
+
+constexpr int64_t kCombineWaves = int64_t(1) << 25;   // most waves of a launch
 
 struct Eight {
   f32x4_t lo, hi;
@@ -413,9 +415,9 @@ struct Raw8<false> {
 
 template <bool Y16, bool OUT16>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t i = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (i >= a.waves) return;
-  const int64_t t = a.waves <= 0xFFFFFFFFll ? static_cast<uint32_t>(i) / static_cast<uint32_t>(a.parts) : i / a.parts;
+  const int64_t t = i / static_cast<uint32_t>(a.parts);
   const int unit = 64 * static_cast<int>(i - t * a.parts) + (threadIdx.x & 63);
   if (unit >= a.M8) return;
   const int col = 8 * unit;
@@ -557,26 +559,30 @@ usw_status usw_expert_combine(const void* Y, int32_t y_type, int32_t S, int32_t 
   if (T == 0) return USW_OK;
   CombineArgs a{};
   a.y = Y;
-  a.pos = pos;
-  a.weights = weights;
-  a.res = res;
-  a.out = out;
   a.ld_res = ld_res;
   a.S = S;
   a.M8 = M / 8;
   a.k = k;
   a.parts = (a.M8 + 63) / 64;
-  a.waves = static_cast<int64_t>(T) * a.parts;
-  const int64_t blocks = (a.waves + 3) / 4;
-  if (blocks >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
-  const dim3 grid(static_cast<unsigned>(blocks));
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool y16 = y_type == USW_OUT_F16, o16 = out_type == USW_OUT_F16;
-  if (y16 && o16) combine_kernel<true, true><<<grid, 256, 0, s>>>(a);
-  else if (y16) combine_kernel<true, false><<<grid, 256, 0, s>>>(a);
-  else if (o16) combine_kernel<false, true><<<grid, 256, 0, s>>>(a);
-  else combine_kernel<false, false><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError() == hipSuccess ? USW_OK : USW_ERR_HIP;
+  // As many tokens a launch as stay under its 2^32 threads.
+  const int64_t most = std::max<int64_t>(1, kCombineWaves / a.parts);
+  for (int64_t t0 = 0; t0 < T; t0 += most) {
+    const int64_t n = std::min(most, T - t0);
+    a.pos = pos + t0 * k;
+    a.weights = weights + t0 * k;
+    a.res = res ? res + t0 * ld_res : nullptr;
+    a.out = static_cast<uint8_t*>(out) + t0 * M * (o16 ? 2 : 4);
+    a.waves = static_cast<uint32_t>(n * a.parts);
+    const dim3 grid((a.waves + 3) / 4);
+    if (y16 && o16) combine_kernel<true, true><<<grid, 256, 0, s>>>(a);
+    else if (y16) combine_kernel<true, false><<<grid, 256, 0, s>>>(a);
+    else if (o16) combine_kernel<false, true><<<grid, 256, 0, s>>>(a);
+    else combine_kernel<false, false><<<grid, 256, 0, s>>>(a);
+    if (hipGetLastError() != hipSuccess) return USW_ERR_HIP;
+  }
+  return USW_OK;
 }
 
 }  // extern "C"
