@@ -673,7 +673,8 @@ usw_status usw_spmm_fused_workspace(const usw_fmt* fmt, int32_t N, int32_t split
  * else that the call reads.
  * Errors: as usw_spmm_ex, and BAD_DTYPE (act), BAD_SHAPE (a stride below M or
  * above 2^20, with more outputs than that 2^22, reserved), MISALIGNED (scales, bias, mul or res not 16-byte
- * aligned, a stride that is no multiple of 8), UNSUPPORTED (M > 2^22).
+ * aligned, a stride that is no multiple of 8), UNSUPPORTED (M > 2^22, a launch
+ * of 2^32 threads).
  */
 usw_status usw_spmm_fused(const usw_fmt* fmt, const uint16_t* X, void* Y, int32_t y_type, int32_t N,
                           const usw_epilogue* ep, int32_t splits, void* ws, size_t ws_bytes, void* stream);
@@ -713,7 +714,7 @@ usw_status usw_expert_spmm_workspace(const usw_expert_fmt* fmt, int32_t S, size_
  * rows, not wrong accesses.  S = 0 does nothing.
  * Errors: as usw_spmm_fused; BAD_N (S or T negative, T < S without rows, T = 0
  * with S > 0), BAD_SHAPE (E < 1, nnz or values_bytes impossible), UNSUPPORTED
- * (E > 1024).
+ * (E > 1024 too).
  */
 usw_status usw_expert_spmm(const usw_expert_fmt* fmt, const uint16_t* X, int32_t T, const int32_t* slots,
                            const int32_t* rows, int32_t S, void* Y, int32_t y_type, const usw_epilogue* ep, void* ws,
@@ -737,8 +738,8 @@ usw_status usw_expert_route_workspace(int32_t T, int32_t E, int32_t k, size_t* b
  *   pos:     out int32 [T][k], the slot of each choice; -1 where none was left.
  * Deterministic.  T = 0 writes slots only.
  * Errors: NULL_ARG, BAD_N (T < 0), BAD_SHAPE (E < 1, k < 1, k > E, ld < E or
- * > 2^31), BAD_DTYPE, UNSUPPORTED (E > 1024, k > 16, T k >= 2^31),
- * MISALIGNED, WORKSPACE, HIP.
+ * > 2^31), BAD_DTYPE, UNSUPPORTED (E > 1024, k > 16, T k >= 2^31,
+ * T > 2^28 - 64), MISALIGNED, WORKSPACE, HIP.
  */
 usw_status usw_expert_route(const void* logits, int32_t l_type, int64_t ld, int32_t T, int32_t E, int32_t k,
                             int32_t renormalize, int32_t* ids, float* weights, int32_t* slots, int32_t* rows,

@@ -31,6 +31,12 @@ constexpr int64_t kMaxLd = int64_t(1) << 20;
 // the passes address the operands with 64 bits.
 constexpr int64_t kMaxM = int64_t(1) << 22;
 
+// HIP's limit on a launch is 2^32 threads.
+bool launchable(int64_t workgroups, bool ring) {
+  return workgroups < (int64_t(1) << 32) / (ring ? kRingThreads : DefaultCfg::kThreadsPerGroup);
+}
+static_assert(DefaultCfg::kThreadsPerGroup == 256 && DefaultCfg8::kThreadsPerGroup == 256, "every per-wave configuration alike");
+
 // Checks an epilogue for rows of M outputs and fills the kernels' copy.
 usw_status make_epilogue(const usw_epilogue* ep, int64_t M, int32_t y_type, Epilogue* e) {
   *e = Epilogue{nullptr, nullptr, nullptr, M, M, USW_ACT_NONE, y_type == USW_OUT_F16 ? 1 : 0};
@@ -114,6 +120,7 @@ usw_status fused_impl(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_ty
   st = make_epilogue(ep, g.M, y_type, &e);
   if (st) return st;
   const FusedPlan c = plan_fused(f, g, N, splits_req);
+  if (!c.wide && !launchable(g.Gr * std::max(c.p.splits, c.p.rsplits), c.p.ring)) return USW_ERR_UNSUPPORTED;
   if (c.need > 0) {
     if (!ws || ws_bytes < c.need) return USW_ERR_WORKSPACE;
     if (!aligned16(ws)) return USW_ERR_MISALIGNED;
@@ -265,6 +272,8 @@ usw_status expert_impl(const usw_expert_fmt* f, const uint16_t* X, int32_t T, co
   if (st) return st;
   if (S == 0) return USW_OK;
   const ExpertPlan p = plan_expert(f, g, S);
+  const int64_t per = g.Gr * p.splits;   // workgroups of a tile
+  if (!p.wide && !launchable(p.tiles * per, p.ring)) return USW_ERR_UNSUPPORTED;
   if (p.need > 0) {
     if (!ws || ws_bytes < p.need) return USW_ERR_WORKSPACE;
     if (!aligned16(ws)) return USW_ERR_MISALIGNED;
@@ -288,8 +297,6 @@ usw_status expert_impl(const usw_expert_fmt* f, const uint16_t* X, int32_t T, co
     w.e = e;
     return usw::wide_launch(w, g, p.w, ws, stream);
   }
-  const int64_t per = g.Gr * p.splits;
-  if (p.tiles * per >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
   ExpertArgs a{};
   a.bitmaps = f->bitmaps;
   a.offsets = f->offsets;

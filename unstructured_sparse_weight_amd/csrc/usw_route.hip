@@ -40,6 +40,7 @@ constexpr int kMaxRouteExperts = 1024;
 constexpr int kMaxTopK = 16;
 constexpr int kOneTokens = 64;     // tokens the one-workgroup kernel takes
 constexpr int kFineTokens = 4096;  // above that, blocks of 32 tokens up to here, then of 64
+constexpr int kMaxRouteTokens = (1 << 28) - 64;   // their blocks of 64 make less than HIP's 2^32 threads
 constexpr int kAddBlocks = 256;    // most blocks whose counts every block adds itself
 
 struct RouteArgs {
@@ -469,7 +470,7 @@ bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(
 usw_status check_route(int32_t T, int32_t E, int32_t k) {
   if (T < 0) return USW_ERR_BAD_N;
   if (E < 1 || k < 1 || k > E) return USW_ERR_BAD_SHAPE;
-  if (E > kMaxRouteExperts || k > kMaxTopK) return USW_ERR_UNSUPPORTED;
+  if (E > kMaxRouteExperts || k > kMaxTopK || T > kMaxRouteTokens) return USW_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(T) * k >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
   return USW_OK;
 }
