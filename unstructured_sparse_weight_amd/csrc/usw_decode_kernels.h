@@ -92,7 +92,7 @@ struct ExpertArgs : FusedArgs {
   const int64_t* __restrict__ starts;   // [E+1] byte offset of each expert's values
   int64_t values_total;                 // bytes of all experts' values
   int64_t nbt, noff;                    // bitmap words and offsets of one expert
-  int E, S, T, tiles, lg_chunk, Gr;
+  int E, S, T, lg_chunk, Gr;
 };
 template <>
 struct ArgTraits<ExpertArgs> {

@@ -323,7 +323,6 @@ usw_status expert_impl(const usw_expert_fmt* f, const uint16_t* X, int32_t T, co
   a.E = f->E;
   a.S = S;
   a.T = T;
-  a.tiles = static_cast<int>(p.tiles);
   a.lg_chunk = p.lg_chunk;
   a.Gr = static_cast<int>(g.Gr);
   launch_pass(a, p.ring, i4, p.lean, 1 << (p.lg_chunk - 4), e.f16out, dim3(static_cast<unsigned>(p.tiles * per)),
