@@ -657,7 +657,9 @@ typedef struct usw_epilogue {
  * their own.  A call has no counters or at least 64 KiB of them, and uses the
  * first 64 KiB of its workspace for nothing else, so calls of any sizes may
  * take turns on a workspace whose first 64 KiB were zeroed once, while none
- * reports more counter bytes than that.
+ * reports more counter bytes than that.  A call that does needs them zeroed
+ * after every call that reports fewer or none: those may have left sums or
+ * weights from 64 KiB on.
  */
 usw_status usw_spmm_fused_workspace(const usw_fmt* fmt, int32_t N, int32_t splits, size_t* bytes,
                                     size_t* counter_bytes);
@@ -666,15 +668,15 @@ usw_status usw_spmm_fused_workspace(const usw_fmt* fmt, int32_t N, int32_t split
  * Y [N][M] as above, X [N][K] fp16.  As usw_spmm_ex otherwise (layouts,
  * alignment, splits, workspace, stream, determinism).  Few rows take the
  * decode kernels in passes of up to 128; from 65 rows (weights of more than
- * 2^22 elements 129, fp16 of more than 2^26 193) the weight is expanded once to dense fp16 in the workspace (2 M K
- * bytes) and multiplied there, unless splits > 0.  ep may be NULL: no
- * epilogue.  ep and the struct it points to are read during the call.  Y may
- * be the residual itself (same address, ld_res = M); it may overlap nothing
- * else that the call reads.
- * Errors: as usw_spmm_ex, and BAD_DTYPE (act), BAD_SHAPE (a stride below M or
- * above 2^20, with more outputs than that 2^22, reserved), MISALIGNED (scales, bias, mul or res not 16-byte
- * aligned, a stride that is no multiple of 8), UNSUPPORTED (M > 2^22, a launch
- * of 2^32 threads).
+ * 2^22 elements 129, fp16 of more than 2^26 193) the weight is expanded once
+ * to dense fp16 in the workspace (2 M K bytes) and multiplied there, unless
+ * splits > 0 or M > 2^20.  ep may be NULL: no epilogue.  ep and the struct it
+ * points to are read during the call.  Y may be the residual itself (same
+ * address, ld_res = M); it may overlap nothing else that the call reads.
+ * Errors: as usw_spmm_ex, and BAD_DTYPE (act), BAD_SHAPE (reserved; a stride
+ * below M or above 2^20, where M > 2^20 above 2^22), MISALIGNED (scales, bias,
+ * mul or res not 16-byte aligned, a stride that is no multiple of 8),
+ * UNSUPPORTED (M > 2^22, a launch of 2^32 threads).
  */
 usw_status usw_spmm_fused(const usw_fmt* fmt, const uint16_t* X, void* Y, int32_t y_type, int32_t N,
                           const usw_epilogue* ep, int32_t splits, void* ws, size_t ws_bytes, void* stream);
@@ -695,8 +697,10 @@ typedef struct usw_expert_fmt {
 } usw_expert_fmt;
 
 /* Workspace of usw_expert_spmm for S slots, with usw_spmm_fused_workspace's
- * rules.  With 128 slots an expert or more it holds expanded weights, up to
- * 1 GiB of them (or one) at a time. */
+ * rules.  Ask for it: from a mean of S / min(E, S) slots an expert (128 where
+ * the weights have up to 2^26 elements in all, else 224; 80 with K up to 256,
+ * 32 with K = 64; never with M > 2^20) it holds expanded weights, 2 M K bytes
+ * each, up to 1 GiB of them (or one) at a time. */
 usw_status usw_expert_spmm_workspace(const usw_expert_fmt* fmt, int32_t S, size_t* bytes, size_t* counter_bytes);
 
 /*
@@ -710,8 +714,9 @@ usw_status usw_expert_spmm_workspace(const usw_expert_fmt* fmt, int32_t S, size_
  *   rows:  device int32 [S] or NULL; entries from slots[E] on are not read.
  *   ep:    as usw_spmm_fused, with a bias per expert; mul and res have a row
  *          per slot.
- * Runs, rows and starts are clamped to the buffers: wrong ones give wrong
- * rows, not wrong accesses.  S = 0 does nothing.
+ * Runs, rows and starts are clamped to the buffers: wrong ones, runs that
+ * overlap or fall among them, give wrong rows, not wrong accesses.  S = 0 does
+ * nothing.
  * Errors: as usw_spmm_fused; BAD_N (S or T negative, T < S without rows, T = 0
  * with S > 0), BAD_SHAPE (E < 1, nnz or values_bytes impossible), UNSUPPORTED
  * (E > 1024 too).

@@ -207,6 +207,10 @@ usw_status check_expert(const usw_expert_fmt* f, int32_t y_type, int32_t S, usw:
 ExpertPlan plan_expert(const usw_expert_fmt* f, const usw::Geometry& g, int32_t S) {
   ExpertPlan p{};
   const bool i4 = f->val_type == USW_VAL_I4;
+  // By the bank's mean density, the one that the host has.  An expert above
+  // 62% in a bank below 55% takes the unpipelined path (8 of 11008x4096 with 8
+  // rows each, seven 50% and one 70% dense: 149 us; the six-chunk kernels 94,
+  // and all at 54% 100).
   p.lean = !i4 && static_cast<double>(f->nnz) <= 0.55 * static_cast<double>(f->E) * g.M * g.K;
   const int64_t active = std::min<int64_t>(f->E, S);
   const int64_t mean = S / std::max<int64_t>(1, active);

@@ -12,7 +12,8 @@
 Argument marshalling only, like the rest of the binding: the work runs in
 libusw's kernels (include/usw.h), on torch's current stream or ``stream``.
 Calls may be captured in a HIP graph; a captured call has a workspace of its
-own, in the graph's memory pool.
+own, in the graph's memory pool.  The others share one a stream, which grows
+to the largest call's and is kept until ``release_workspaces()``.
 """
 from __future__ import annotations
 
@@ -244,8 +245,9 @@ def spmm_fused(enc, x, bias=None, act: str = "none", mul=None, residual=None, y=
     x [N][K] fp16; bias [M], mul [N][M], residual [N][M] fp16, each optional;
     act "none", "relu", "gelu", "gelu_tanh" or "silu".  The sums and the
     epilogue are fp32 and Y (fp16, or ``out_dtype`` float32) is rounded once.
-    ``y`` may be ``residual`` itself.  mul and residual may be rows of a wider
-    tensor.  Encodings have 64x64 GroupTiles and fp16 or INT4 values.
+    ``y`` may be ``residual`` itself, and may overlap nothing else that the
+    call reads.  mul and residual may be rows of a wider tensor.  Encodings
+    have 64x64 GroupTiles and fp16 or INT4 values.
     """
     dev = enc.device
 
