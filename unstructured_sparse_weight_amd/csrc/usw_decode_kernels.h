@@ -403,9 +403,10 @@ __device__ __forceinline__ uint32_t bitmap_prefix_reg(u32x2_t bm) {
 //   kStep: one token block with fp16 output, where the subtractions would cost
 //     2 to 6% and the matrix cores idle: a product with the offset's negative
 //     goes into the same accumulator before each step's own, so no more than
-//     72 sum|x| of one step of 32 columns is ever in it (20480x5120 N = 8:
-//     19.3 us collected, 19.8 so, 20.4 by subtractions; 11008x4096 N = 16:
-//     15.7 / 15.9 / 16.4).
+//     72 sum|x| of one step of 32 columns is ever in it: an x leaves at most
+//     72 2^-24 |x| = 4e-6 |x| for each rounding of its step, in units where its
+//     codes are whole numbers (20480x5120 N = 8: 19.3 us collected, 19.8 so,
+//     20.4 by subtractions; 11008x4096 N = 16: 15.7 / 15.9 / 16.4).
 enum class CodeOffset { kCollect, kEach, kStep };
 
 // Rebuild and multiply fragments f = F0 .. F1-1 (both ks) of a GroupTile
