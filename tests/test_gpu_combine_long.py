@@ -14,7 +14,7 @@ import unstructured_sparse_weight_amd as usw  # noqa: E402
 DEV = "cuda:0"
 
 
-@pytest.mark.parametrize("T,M,residual", [((1 << 26) + 5, 8, False), ((1 << 25) + 3, 16, True), ((1 << 24) + 1, 1032, False)])
+@pytest.mark.parametrize("T,M,residual", [((1 << 26) + 5, 8, False), ((1 << 25) + 3, 16, True), ((1 << 24) + 1, 520, False)])
 def test_many_tokens(T, M, residual):
     """Whole numbers: exact.  Tokens read rows of a short Y in an uneven order."""
     S = 251
@@ -25,10 +25,10 @@ def test_many_tokens(T, M, residual):
     res = torch.randint(-9, 10, (T, M), device=DEV, generator=g).half() if residual else None
     print(f"[combine] T={T} M={M}", file=sys.stderr, flush=True)
     out = usw.expert_combine(y, pos, w, residual=res)
-    for a in range(0, T, 1 << 22):
-        p = pos[a:a + (1 << 22), 0].long()
+    for a in range(0, T, 1 << 21):
+        p = pos[a:a + (1 << 21), 0].long()
         live = ((p >= 0) & (p < S)).half()[:, None]
-        want = y[p.clamp(0, S - 1)] * live * w[a:a + (1 << 22)].half()
+        want = y[p.clamp(0, S - 1)] * live * w[a:a + (1 << 21)].half()
         if residual:
-            want = want + res[a:a + (1 << 22)]
-        assert torch.equal(out[a:a + (1 << 22)], want), a
+            want = want + res[a:a + (1 << 21)]
+        assert torch.equal(out[a:a + (1 << 21)], want), a
