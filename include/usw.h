@@ -862,8 +862,9 @@ usw_status usw_spmm_gated_backward_workspace(const usw_fmt* gate, const usw_fmt*
  * above.  The products take dg and du rounded to fp16 (more than 32 rows) or to
  * an fp16 value and the fp16 remainder (up to 32), the biases' sums unrounded.
  * So dg and du share fp16's range with their results: a loss is scaled as for
- * any fp16 gradient.  ReLU's slope at 0 is 0.  Rules and errors as
- * usw_spmm_backward.
+ * any fp16 gradient.  Infinities of X and of fp16 weights stay infinite where
+ * |dg| and |du| are 2^-24 and more.  ReLU's slope at 0 is 0.  Rules and errors
+ * as usw_spmm_backward.
  */
 usw_status usw_spmm_gated_backward(const usw_fmt* gate, const usw_fmt* up, const uint16_t* X, int32_t N,
                                    const usw_gated_grad* grad, void* ws, size_t ws_bytes, void* stream);

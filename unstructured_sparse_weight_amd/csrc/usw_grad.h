@@ -66,6 +66,20 @@ __device__ __forceinline__ float scale_rest(float s) {
   return s * __uint_as_float((254u << 23) - __float_as_uint(scale_power(s)));   // by 2^-e, exact
 }
 
+// v with the largest numbers for infinities and NaN: what remainders of d are
+// multiplied with.  An infinity is in the product with d itself, where a
+// remainder of zero, or of the other sign, would make a NaN of it.  As whole
+// numbers +inf and its NaN are the largest signed ones, -inf and its the largest
+// unsigned ones.  For the values it costs half a percent (pairs of 11008x4096 N = 8
+// 68.3 / 68.9 us).
+__device__ __forceinline__ half8_t finite(half8_t v) {
+  typedef short s16x8_t __attribute__((ext_vector_type(8)));
+  typedef unsigned short u16x8_t __attribute__((ext_vector_type(8)));
+  const s16x8_t up = __builtin_elementwise_min(__builtin_bit_cast(s16x8_t, v), s16x8_t{} + static_cast<short>(0x7BFF));
+  return __builtin_bit_cast(half8_t, __builtin_elementwise_min(__builtin_bit_cast(u16x8_t, up),
+                                                               u16x8_t{} + static_cast<unsigned short>(0xFBFF)));
+}
+
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kTrLd = 72;                     // halves of a row of a tile of 64 columns in LDS: rows 144 bytes apart

@@ -92,17 +92,18 @@ __device__ __forceinline__ void column_mma(const u32x4_t (&x)[NB], const uint8_t
   }
   wave_sync();
 }
-// And with its remainders.
-template <int NB>
+// And with its remainders.  GUARD: infinite weights are left to d itself.
+template <int NB, bool GUARD>
 __device__ __forceinline__ void column_mma(const u32x4_t (&x)[NB], const u32x4_t (&lo)[NB], const uint8_t* tile,
                                            f32x4_t (&acc)[4][NB], int lane) {
 #pragma unroll
   for (int f = 0; f < 4; ++f) {
     const half8_t w = read_column(tile, lane, 16 * f);
+    const half8_t wf = GUARD ? finite(w) : w;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       acc[f][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(half8_t, x[nb]), acc[f][nb], 0, 0, 0);
-      acc[f][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, __builtin_bit_cast(half8_t, lo[nb]), acc[f][nb], 0, 0, 0);
+      acc[f][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, __builtin_bit_cast(half8_t, lo[nb]), acc[f][nb], 0, 0, 0);
     }
   }
   wave_sync();
@@ -196,47 +197,49 @@ __device__ __forceinline__ void column_body(const ColumnArgs& a, uint8_t* lds, u
   auto write_tab = [&](const Slot<NB, I4, CH>& s) {
     tab_write(tab, s.bm, bitmap_prefix_reg(s.bm) + s.delta + vb_elems, lane);
   };
-  if (cnt <= 0) {
-    // nothing to stream
-  } else if (widest > VT::kFastLimit) {
-    if constexpr (!I4) {
-      // As in the decode kernel: the values of half a GroupTile at a time.
-      for (int c = c_begin; c < c_end; ++c) {
-        Slot<NB, I4, CH> s0;
-        uint32_t none[4];
-        load_w(s0, none, c);
-        const int e = c >= a.rows ? 1 : 0;
-        const uint8_t* values = e ? a.wvalues[1] : a.wvalues[0];
-        const uint64_t top = (e ? a.walloc[1] : a.walloc[0]) - 16;
-        const uint32_t o0 = __builtin_amdgcn_readlane(first, c - c_begin), o1 = __builtin_amdgcn_readlane(past, c - c_begin);
-        const uint32_t excl = bitmap_prefix_reg(s0.bm);
-        const uint32_t mid = __builtin_amdgcn_readlane(excl, 32);
+  // As in the decode kernel: the values of half a GroupTile at a time.
+  auto by_halves = [&](auto guard) {
+    constexpr bool GUARD = decltype(guard)::value;
+    for (int c = c_begin; c < c_end; ++c) {
+      Slot<NB, I4, CH> s0;
+      uint32_t none[4];
+      load_w(s0, none, c);
+      const int e = c >= a.rows ? 1 : 0;
+      const uint8_t* values = e ? a.wvalues[1] : a.wvalues[0];
+      const uint64_t top = (e ? a.walloc[1] : a.walloc[0]) - 16;
+      const uint32_t o0 = __builtin_amdgcn_readlane(first, c - c_begin), o1 = __builtin_amdgcn_readlane(past, c - c_begin);
+      const uint32_t excl = bitmap_prefix_reg(s0.bm);
+      const uint32_t mid = __builtin_amdgcn_readlane(excl, 32);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          u32x4_t d[NB];
-          load_d(d, c, h, 0);
-          const uint32_t hs = o0 + (h ? mid : 0u), he = h ? o1 : o0 + mid;
-          const uint64_t a0 = min(chunk_start<I4>(hs), top);
-          const uint32_t delta = chunk_delta<I4>(hs, a0);
-          const uint32_t nch = min(chunk_count<I4>(he, a0), static_cast<uint32_t>((VT::kVbuf - 16) / 16));
-          const uint32_t last = static_cast<uint32_t>((top - a0) >> 4);
-          const u32x4_t* src = reinterpret_cast<const u32x4_t*>(values + a0);
-          for (uint32_t ch = lane; ch < nch; ch += 64) reinterpret_cast<u32x4_t*>(vb)[ch] = src[min(ch, last)];
-          // Entries of the other half get bases that are never read.
-          tab_write(tab, s0.bm, excl - (h ? mid : 0u) + delta + vb_elems, lane);
-          wave_sync();
-          if (h == 0) column_rows<I4, 0>(smem, tab, lut, tile, none, lm, lane);
-          else column_rows<I4, 1>(smem, tab, lut, tile, none, lm, lane);
-          if constexpr (LO) {
-            u32x4_t dlo[NB];
-            load_d(dlo, c, h, a.lo);
-            column_mma<NB>(d, dlo, tile, acc, lane);
-          } else {
-            column_mma<NB>(d, tile, acc, lane);
-          }
+      for (int h = 0; h < 2; ++h) {
+        u32x4_t d[NB];
+        load_d(d, c, h, 0);
+        const uint32_t hs = o0 + (h ? mid : 0u), he = h ? o1 : o0 + mid;
+        const uint64_t a0 = min(chunk_start<I4>(hs), top);
+        const uint32_t delta = chunk_delta<I4>(hs, a0);
+        const uint32_t nch = min(chunk_count<I4>(he, a0), static_cast<uint32_t>((VT::kVbuf - 16) / 16));
+        const uint32_t last = static_cast<uint32_t>((top - a0) >> 4);
+        const u32x4_t* src = reinterpret_cast<const u32x4_t*>(values + a0);
+        for (uint32_t ch = lane; ch < nch; ch += 64) reinterpret_cast<u32x4_t*>(vb)[ch] = src[min(ch, last)];
+        // Entries of the other half get bases that are never read.
+        tab_write(tab, s0.bm, excl - (h ? mid : 0u) + delta + vb_elems, lane);
+        wave_sync();
+        if (h == 0) column_rows<I4, 0>(smem, tab, lut, tile, none, lm, lane);
+        else column_rows<I4, 1>(smem, tab, lut, tile, none, lm, lane);
+        if constexpr (LO) {
+          u32x4_t dlo[NB];
+          load_d(dlo, c, h, a.lo);
+          column_mma<NB, GUARD>(d, dlo, tile, acc, lane);
+        } else {
+          column_mma<NB>(d, tile, acc, lane);
         }
       }
     }
+  };
+  if (cnt <= 0) {
+    // nothing to stream
+  } else if (widest > VT::kFastLimit) {
+    if constexpr (!I4) by_halves(std::false_type{});
   } else if constexpr (NB > 2) {
     // Registers for three waves per SIMD (more than 64 tokens two): half a
     // GroupTile's d at a time, and the next weight in one slot, asked for where
@@ -289,10 +292,10 @@ __device__ __forceinline__ void column_body(const ColumnArgs& a, uint8_t* lds, u
       slot_commit(s[cur].s, vb, lane);
       wave_sync();
       column_rows<I4, 0>(smem, tab, lut, tile, s[cur].scale, lm, lane);
-      if constexpr (LO) column_mma<NB>(s[cur].d[0], s[cur].lo[0], tile, acc, lane);
+      if constexpr (LO) column_mma<NB, false>(s[cur].d[0], s[cur].lo[0], tile, acc, lane);
       else column_mma<NB>(s[cur].d[0], tile, acc, lane);
       column_rows<I4, 1>(smem, tab, lut, tile, s[cur].scale, lm, lane);
-      if constexpr (LO) column_mma<NB>(s[cur].d[1], s[cur].lo[1], tile, acc, lane);
+      if constexpr (LO) column_mma<NB, false>(s[cur].d[1], s[cur].lo[1], tile, acc, lane);
       else column_mma<NB>(s[cur].d[1], tile, acc, lane);
       write_tab(s[cur ^ 1].s);
     };
@@ -302,6 +305,26 @@ __device__ __forceinline__ void column_body(const ColumnArgs& a, uint8_t* lds, u
       step(c + 1, 1);
     }
     if (c < c_end) step(c, 0);
+  }
+  if constexpr (LO && !I4) {
+    // An infinite weight times a remainder of zero, or of the other sign than d's,
+    // has left a NaN: the wave's GroupTiles once more, guarded.  Guarding each
+    // weight from the start costs 2 to 4% (pairs of 11008x4096 N = 8 68.3 / 69.7
+    // us, of 20480x5120 N = 20 150 / 156).
+    bool nan = false;
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) nan |= acc[f][nb][i] != acc[f][nb][i];
+    if (__ballot(nan)) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) acc[f][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      by_halves(std::true_type{});
+    }
   }
 
   // Workgroup reduction over waves (fixed order), the last two into the first.
@@ -441,11 +464,12 @@ __device__ __forceinline__ void values_body(const FewValuesArgs& a, uint8_t* sme
 #pragma unroll
       for (int h = 0; h < H; ++h) {
         const half8_t x = read_column(tile + 2 * 32 * h * kTrLd, lane, 16 * n);
+        const half8_t xf = LO ? finite(x) : x;
 #pragma unroll
         for (int f = 0; f < 4; ++f)
 #pragma unroll
           for (int q = 0; q < P; ++q)
-            acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x, d[q][f][h], h + q ? acc[f][n] : f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+            acc[f][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(q ? xf : x, d[q][f][h], h + q ? acc[f][n] : f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
       }
     const Kept<T> k = kept_of<T>(bits, at, nnz, dv, lds, lane);
 #pragma unroll
