@@ -833,9 +833,11 @@ usw_status usw_spmm_backward_workspace(const usw_fmt* fmt, int32_t N, int32_t ou
  * INT4 weights are frozen: no dvalues (UNSUPPORTED).  Their scales multiply dY
  * in part, which rounds it once more, to 11 bits for an fp16 dX of more than 32
  * rows, else to 22.
- * dX may not overlap dY.  X and dY have 16-byte aligned starts.
+ * Outputs may overlap neither each other nor anything that the call reads
+ * (X, dY, the weight, the workspace): dX and dvalues of few rows are one launch.
+ * X and dY have 16-byte aligned starts.
  * Errors: as usw_spmm_fused, and UNSUPPORTED (dvalues of INT4, M or K above
- * 2^20, M K > 2^34, N > 2^22 - 64, N M or N K > 2^35).
+ * 2^20, M K > 2^34, N > 2^22 - 64, N M or N K > 2^35, overlapping outputs).
  */
 usw_status usw_spmm_backward(const usw_fmt* fmt, const uint16_t* X, const uint16_t* dY, int32_t N, void* dX,
                              void* dvalues, float* dbias, int32_t out_type, void* ws, size_t ws_bytes, void* stream);

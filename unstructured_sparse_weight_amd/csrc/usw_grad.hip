@@ -527,6 +527,43 @@ usw_status check_back(const Back& b, usw::Geometry* g) {
   return USW_OK;
 }
 
+// Whether an output lies on another one or on something that the call reads.
+bool outputs_overlap(const Back& b, const usw::Geometry& g, const void* ws, size_t ws_bytes) {
+  struct Span {
+    uintptr_t at;
+    size_t bytes;
+  };
+  Span out[5], in[13];
+  int no = 0, ni = 0;
+  const auto span = [](const void* p, size_t bytes) { return Span{reinterpret_cast<uintptr_t>(p), p ? bytes : 0}; };
+  const size_t size = b.out_type == USW_OUT_F16 ? 2 : 4, rows = static_cast<size_t>(b.N);
+  out[no++] = span(b.dX, rows * g.K * size);
+  in[ni++] = span(b.want_v ? b.X : nullptr, rows * g.K * 2);
+  in[ni++] = span(b.dY, rows * g.M * 2);
+  in[ni++] = span(b.g, rows * g.M * 2);
+  in[ni++] = span(b.u, rows * g.M * 2);
+  in[ni++] = span(ws, ws_bytes);
+  for (int h = 0; h < b.nw; ++h) {
+    const usw_fmt* f = b.f[h];
+    out[no++] = span(b.dV[h], static_cast<size_t>(f->nnz) * size);
+    out[no++] = span(b.db[h], static_cast<size_t>(g.M) * 4);
+    in[ni++] = span(f->bitmaps, static_cast<size_t>(g.M) * g.K / 8);
+    in[ni++] = span(f->offsets, static_cast<size_t>(g.ngt + 1) * 4);
+    in[ni++] = span(f->values, usw::values_alloc_bytes(f->val_type, f->nnz));
+    in[ni++] = span(b.i4 ? f->scales : nullptr, static_cast<size_t>(g.M) * 2);
+  }
+  const auto meet = [](const Span& a, const Span& c) {
+    return a.bytes > 0 && c.bytes > 0 && a.at < c.at + c.bytes && c.at < a.at + a.bytes;
+  };
+  for (int i = 0; i < no; ++i) {
+    for (int j = 0; j < ni; ++j)
+      if (meet(out[i], in[j])) return true;
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return true;
+  }
+  return false;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 usw_status back_impl(const Back& b, void* ws, size_t ws_bytes, void* stream) {
@@ -550,6 +587,7 @@ usw_status back_impl(const Back& b, void* ws, size_t ws_bytes, void* stream) {
     if (!ws || ws_bytes < p.need) return USW_ERR_WORKSPACE;
     if (!aligned16(ws)) return USW_ERR_MISALIGNED;
   }
+  if (outputs_overlap(b, g, ws, p.need)) return USW_ERR_UNSUPPORTED;
   uint8_t* at = static_cast<uint8_t*>(ws);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool tall_v = b.want_v && !p.few_v;
