@@ -798,7 +798,7 @@ usw_status usw_spmm_gated_workspace(const usw_fmt* gate, const usw_fmt* up, int3
  * else.
  * Errors: as usw_spmm_fused, and BAD_SHAPE, BAD_DTYPE where the two weights'
  * shapes or value types differ, MISALIGNED (a bias, g or u not 16-byte
- * aligned), UNSUPPORTED (M > 2^20, M K > 2^34).
+ * aligned), UNSUPPORTED (M > 2^20, M K > 2^34, a launch of 2^32 threads).
  */
 usw_status usw_spmm_gated(const usw_fmt* gate, const usw_fmt* up, const uint16_t* X, void* Y, int32_t y_type, int32_t N,
                           const usw_gated* opt, void* ws, size_t ws_bytes, void* stream);
@@ -837,7 +837,8 @@ usw_status usw_spmm_backward_workspace(const usw_fmt* fmt, int32_t N, int32_t ou
  * (X, dY, the weight, the workspace): dX and dvalues of few rows are one launch.
  * X and dY have 16-byte aligned starts.
  * Errors: as usw_spmm_fused, and UNSUPPORTED (dvalues of INT4, M or K above
- * 2^20, M K > 2^34, N > 2^22 - 64, N M or N K > 2^35, overlapping outputs).
+ * 2^20, M K > 2^34, N > 2^22 - 64, N M or N K > 2^35, with dvalues N (M + K)
+ * >= 2^36 (N as the next multiple of 64), overlapping outputs).
  */
 usw_status usw_spmm_backward(const usw_fmt* fmt, const uint16_t* X, const uint16_t* dY, int32_t N, void* dX,
                              void* dvalues, float* dbias, int32_t out_type, void* ws, size_t ws_bytes, void* stream);

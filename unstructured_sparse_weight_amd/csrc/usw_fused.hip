@@ -92,7 +92,8 @@ usw_status fused_impl(const usw_fmt* f, const uint16_t* X, void* Y, int32_t y_ty
   st = make_epilogue(ep, g.M, y_type, &e);
   if (st) return st;
   const FusedPlan c = plan_fused(f, g, N, splits_req);
-  if (!c.wide && !launchable(g.Gr * std::max(c.p.splits, c.p.rsplits), c.p.ring)) return USW_ERR_UNSUPPORTED;
+  if (c.wide ? !usw::wide_launchable(c.w) : !launchable(g.Gr * std::max(c.p.splits, c.p.rsplits), c.p.ring))
+    return USW_ERR_UNSUPPORTED;
   if (c.need > 0) {
     if (!ws || ws_bytes < c.need) return USW_ERR_WORKSPACE;
     if (!aligned16(ws)) return USW_ERR_MISALIGNED;
@@ -249,7 +250,7 @@ usw_status expert_impl(const usw_expert_fmt* f, const uint16_t* X, int32_t T, co
   if (S == 0) return USW_OK;
   const ExpertPlan p = plan_expert(f, g, S);
   const int64_t per = g.Gr * p.splits;   // workgroups of a tile
-  if (!p.wide && !launchable(p.tiles * per, p.ring)) return USW_ERR_UNSUPPORTED;
+  if (p.wide ? !usw::wide_launchable(p.w) : !launchable(p.tiles * per, p.ring)) return USW_ERR_UNSUPPORTED;
   if (p.need > 0) {
     if (!ws || ws_bytes < p.need) return USW_ERR_WORKSPACE;
     if (!aligned16(ws)) return USW_ERR_MISALIGNED;

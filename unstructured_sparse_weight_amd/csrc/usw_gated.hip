@@ -485,6 +485,7 @@ usw_status gated_impl(const usw_fmt* gate, const usw_fmt* up, const uint16_t* X,
     o.scales[h] = i4 ? f->scales : nullptr;
   }
   const GatedPlan c = plan_gated(gate, up, g, N);
+  if (c.wide && !usw::wide_launchable(c.w)) return USW_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < c.need) return USW_ERR_WORKSPACE;
   if (!aligned16(ws)) return USW_ERR_MISALIGNED;
   const Epilogue e{nullptr, nullptr, nullptr, g.M, g.M, act, y_type == USW_OUT_F16 ? 1 : 0};
@@ -492,7 +493,6 @@ usw_status gated_impl(const usw_fmt* gate, const usw_fmt* up, const uint16_t* X,
   uint64_t alloc[2];
   for (int h = 0; h < 2; ++h) alloc[h] = usw::values_alloc_bytes(both[h]->val_type, both[h]->nnz);
   if (c.wide) {
-    if (c.w.tiles * c.w.splits >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
     PairExpandArgs x{};
     for (int h = 0; h < 2; ++h) {
       x.bitmaps[h] = both[h]->bitmaps;
@@ -555,6 +555,7 @@ usw_status usw_spmm_gated_workspace(const usw_fmt* gate, const usw_fmt* up, int3
   usw_status st = check_pair(gate, up, USW_OUT_F16, N, &g);
   if (st) return st;
   const GatedPlan c = plan_gated(gate, up, g, N);
+  if (c.wide && !usw::wide_launchable(c.w)) return USW_ERR_UNSUPPORTED;
   *bytes = c.need;
   *counter_bytes = c.cb;
   return USW_OK;

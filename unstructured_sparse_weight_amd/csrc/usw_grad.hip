@@ -48,8 +48,8 @@ namespace {
 
 using namespace usw_dev;
 
-constexpr int64_t kMaxElements = int64_t(1) << 34;   // of a weight, and tokens by outputs: launches stay below
-constexpr int64_t kMaxD = int64_t(1) << 35;          // HIP's 2^32 threads: a thread to 16 of these
+constexpr int64_t kMaxElements = int64_t(1) << 34;   // of a weight, and tokens by outputs or columns: launches
+constexpr int64_t kMaxD = int64_t(1) << 35;          // stay below HIP's 2^32 threads (check_back has d's pass)
 
 // ---------------------------------------------------------------------------
 // d in the orders of the two products
@@ -521,10 +521,17 @@ usw_status check_back(const Back& b, usw::Geometry* g) {
   if (b.i4 && b.want_v) return USW_ERR_UNSUPPORTED;
   // dg and du are rounded to fp16 for the products, so their fp32 results would not be.
   if (b.nw == 2 && b.out_type != USW_OUT_F16) return USW_ERR_UNSUPPORTED;
-  // 64-token chunks are the launches' second dimension, four threads to an
-  // output of 64 tokens.
-  if (b.N > 65535 * kGT || static_cast<int64_t>(b.N) * std::max(g->M, g->K) > kMaxD) return USW_ERR_UNSUPPORTED;
+  // 64-token chunks are the second dimension of d's pass, which takes 256 threads
+  // to one by 64 outputs and, where x's transpose is asked for, by 64 columns.
+  const int64_t chunks = (static_cast<int64_t>(b.N) + kGT - 1) / kGT;
+  if (chunks > 65535 || static_cast<int64_t>(b.N) * std::max(g->M, g->K) > kMaxD ||
+      chunks * (g->Gr + (b.want_v ? g->Gc : 0)) >= int64_t(1) << 24)
+    return USW_ERR_UNSUPPORTED;
   return USW_OK;
+}
+
+bool products_launchable(const Back& b, const BackPlan& p) {
+  return (!b.want_x || p.few || usw::wide_launchable(p.px)) && (!b.want_v || p.few_v || usw::wide_launchable(p.pv));
 }
 
 // Whether an output lies on another one or on something that the call reads.
@@ -581,8 +588,7 @@ usw_status back_impl(const Back& b, void* ws, size_t ws_bytes, void* stream) {
       return USW_ERR_MISALIGNED;
   }
   const BackPlan p = plan_back(b, g);
-  if ((b.want_x && !p.few && p.px.tiles * p.px.splits >= (int64_t(1) << 31)) || (b.want_v && !p.few_v && p.pv.tiles * p.pv.splits >= (int64_t(1) << 31)))
-    return USW_ERR_UNSUPPORTED;
+  if (!products_launchable(b, p)) return USW_ERR_UNSUPPORTED;
   if (p.need > 0) {
     if (!ws || ws_bytes < p.need) return USW_ERR_WORKSPACE;
     if (!aligned16(ws)) return USW_ERR_MISALIGNED;
@@ -692,6 +698,7 @@ usw_status workspace_of(Back b, int32_t grads, size_t* bytes, size_t* counter_by
   usw_status st = check_back(b, &g);
   if (st) return st;
   const BackPlan p = plan_back(b, g);
+  if (!products_launchable(b, p)) return USW_ERR_UNSUPPORTED;
   *bytes = p.need;
   *counter_bytes = p.cb;
   return USW_OK;

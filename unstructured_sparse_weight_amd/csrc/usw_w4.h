@@ -14,7 +14,7 @@ constexpr int kW4Rows = 16, kW4Cols = 128;   // a tile
 inline int w4_tiles(int64_t K) { return static_cast<int>((K + kW4Cols - 1) / kW4Cols); }   // of a row block
 
 // M at most 2^20 keeps a tile's rows of outputs within 32-bit addresses, M K
-// at most 2^34 every launch below HIP's 2^32 threads.
+// at most 2^34 the encoder's and the expansion's launches below HIP's 2^32 threads.
 inline usw_status check_w4_shape(int64_t M, int64_t K, int32_t group) {
   if (M <= 0 || K <= 0 || M % kW4Rows || K % 64) return USW_ERR_BAD_SHAPE;
   if (group != 32 && group != 64 && group != 128) return USW_ERR_BAD_SHAPE;

@@ -400,6 +400,7 @@ usw_status w4_impl(const usw_w4_fmt* f, const uint16_t* X, void* Y, int32_t y_ty
   st = make_epilogue(ep, f->M, y_type, &e);
   if (st) return st;
   const W4Plan p = plan_w4(f, N);
+  if (p.wide && !usw::wide_launchable(p.w)) return USW_ERR_UNSUPPORTED;
   if (p.need > 0) {
     if (!ws || ws_bytes < p.need) return USW_ERR_WORKSPACE;
     if (!aligned16(ws)) return USW_ERR_MISALIGNED;
@@ -461,6 +462,7 @@ usw_status usw_w4_matmul_workspace(const usw_w4_fmt* f, int32_t N, size_t* bytes
   usw_status st = check_w4(f, USW_OUT_F16, N);
   if (st) return st;
   const W4Plan p = plan_w4(f, N);
+  if (p.wide && !usw::wide_launchable(p.w)) return USW_ERR_UNSUPPORTED;
   *bytes = p.need;
   *counter_bytes = p.cb;
   return USW_OK;

@@ -49,6 +49,13 @@ struct WidePlan {
 // columns are shared then): the gradient of 11008x4096 pairs, N = 2048, whose
 // product has 128 of them over 344 columns, 853 us with large, 925 with medium.
 WidePlan wide_plan(const Geometry& g, int32_t E, int32_t S, bool lone = false);
+
+// Whether the plan's product is a launch: less than HIP's 2^32 threads, 256 of
+// them to each workgroup of the small and medium tiles, whose number is rounded up
+// to a multiple of 8; the large tiles' launch is of fixed size, their numbers 32-bit.
+inline bool wide_launchable(const WidePlan& p) {
+  return p.tiling == 0 ? p.tiles < (int64_t(1) << 31) : p.tiles * p.splits <= (int64_t(1) << 24) - 8;
+}
 usw_status wide_launch(const WideCall& c, const Geometry& g, const WidePlan& p, void* ws, void* stream);
 
 // The product alone, Y [rows][g.M] from X [rows][g.K] and dense fragments that

@@ -119,7 +119,7 @@ usw_status wide_launch(const WideCall& c, const Geometry& g, const WidePlan& p, 
   a.e = c.e;
   a.T = c.T;
   a.i4 = c.val_type == USW_VAL_I4;
-  if (p.tiles * p.splits >= (int64_t(1) << 31) || g.ngt / kExpandWaves >= (int64_t(1) << 31) - 1) return USW_ERR_UNSUPPORTED;
+  if (!wide_launchable(p) || g.ngt / kExpandWaves >= (int64_t(1) << 31) - 1) return USW_ERR_UNSUPPORTED;
   const unsigned gx = static_cast<unsigned>((g.ngt + kExpandWaves - 1) / kExpandWaves);
   for (int e0 = 0; e0 < c.E; e0 += p.group) {
     const int e1 = std::min(c.E, e0 + p.group);
@@ -136,7 +136,7 @@ usw_status wide_launch(const WideCall& c, const Geometry& g, const WidePlan& p, 
 
 usw_status wide_multiply(const Geometry& g, const WidePlan& p, int32_t rows, const uint16_t* X, void* Y,
                          const usw_dev::Epilogue& e, const void* dense, void* ws, void* stream) {
-  if (p.tiles * p.splits >= (int64_t(1) << 31)) return USW_ERR_UNSUPPORTED;
+  if (!wide_launchable(p)) return USW_ERR_UNSUPPORTED;
   WideArgs a{};
   fill_wide(a, p, g, rows, dense, ws);
   a.X = X;
