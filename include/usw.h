@@ -814,8 +814,8 @@ usw_status usw_spmm_gated(const usw_fmt* gate, const usw_fmt* up, const uint16_t
 #define USW_GRAD_VALUES 2   /* the kept values' (either weight's) */
 #define USW_GRAD_BIAS 4     /* and the bias's (either one's) */
 
-/* Workspace of usw_spmm_backward and its leading counter bytes, with
- * usw_spmm_fused_workspace's rules. */
+/* Workspace of usw_spmm_backward (never 0: the counters' 64 KiB at least) and its
+ * leading counter bytes, with usw_spmm_fused_workspace's rules. */
 usw_status usw_spmm_backward_workspace(const usw_fmt* fmt, int32_t N, int32_t out_type, int32_t grads, size_t* bytes,
                                        size_t* counter_bytes);
 
@@ -856,6 +856,7 @@ typedef struct usw_gated_grad {
   int32_t reserved;           /* must be 0 */
 } usw_gated_grad;
 
+/* As usw_spmm_backward_workspace. */
 usw_status usw_spmm_gated_backward_workspace(const usw_fmt* gate, const usw_fmt* up, int32_t N, int32_t grads,
                                              size_t* bytes, size_t* counter_bytes);
 

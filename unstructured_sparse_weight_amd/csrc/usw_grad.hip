@@ -589,10 +589,8 @@ usw_status back_impl(const Back& b, void* ws, size_t ws_bytes, void* stream) {
   }
   const BackPlan p = plan_back(b, g);
   if (!products_launchable(b, p)) return USW_ERR_UNSUPPORTED;
-  if (p.need > 0) {
-    if (!ws || ws_bytes < p.need) return USW_ERR_WORKSPACE;
-    if (!aligned16(ws)) return USW_ERR_MISALIGNED;
-  }
+  if (!ws || ws_bytes < p.need) return USW_ERR_WORKSPACE;
+  if (!aligned16(ws)) return USW_ERR_MISALIGNED;
   if (outputs_overlap(b, g, ws, p.need)) return USW_ERR_UNSUPPORTED;
   uint8_t* at = static_cast<uint8_t*>(ws);
   hipStream_t s = static_cast<hipStream_t>(stream);
