@@ -342,17 +342,22 @@ usw_status check_w4(const usw_w4_fmt* f, int32_t y_type, int32_t N) {
 // Row blocks of a workgroup: more of them share x's way through LDS, fewer spread
 // the codes over the compute units.  A workgroup's time is about R + share, and
 // each round of one to a compute unit adds that (MI355X, R = 1 / 2 / 3 / 4 / 5, us;
-// N = 16: 20480x5120 22.7 / 19.1 / 16.8 / 21.2 / 16.0, 16384x4096 16.6 / 14.0 / 14.5
-// / 12.9 / 14.5, 8192x8192 16.0 / 11.7 / 13.4 / 15.7 / 18.6; N = 32: 20480x5120 33.2 /
+// N = 16: 20480x5120 21.8 / 18.0 / 16.0 / 20.2 / 15.1, 16384x4096 14.9 / 10.8 / 12.7
+// / 10.7 / 13.5, 8192x8192 16.0 / 11.1 / 12.7 / 15.1 / 17.9; N = 32: 20480x5120 33.2 /
 // 28.3 / 24.2 / 26.3 / 21.5, 11008x4096 19.0 / 15.5 / 12.9 / 13.1 / 16.7; N = 64:
 // 20480x5120 62.8 / 42.5 / 36.7 / 41.4 / 29.1, 11008x4096 33.0 / 23.7 / 17.6 / 19.9 /
 // 22.0).  More than five are behind two rounds of fewer: 28672x4096 N = 4 18.1 with
-// three, 18.5 with seven.
-int row_blocks(int64_t blocks, double share) {
+// three, 18.5 with seven.  Of up to 16 rows, more than one round is of workgroups of
+// three or four (128256x4096 N = 1 48.8 / 50.2, with five 53.6, N = 16 60.2 / 57.3 and
+// 59.3).
+constexpr int kComputeUnits = 256;
+int row_blocks(int64_t blocks, int NB) {
+  const double share = NB == 1 ? 1.5 : NB == 2 ? 2.5 : 4.0;
+  const int most = NB == 1 && blocks > 5 * kComputeUnits ? 4 : 5;
   int best = 1;
   double least = 0;
-  for (int r = 1; r <= 5; ++r) {
-    const double rounds = static_cast<double>((blocks + 256 * r - 1) / (256 * r));
+  for (int r = 1; r <= most; ++r) {
+    const double rounds = static_cast<double>((blocks + kComputeUnits * r - 1) / (kComputeUnits * r));
     const double cost = rounds * (r + share);
     if (r == 1 || cost < least) {
       best = r;
@@ -368,25 +373,39 @@ void launch_w4_as(const W4Args& a, hipStream_t s) {
   w4_kernel<R, NB, W, D><<<(blocks + R - 1) / R, 64 * W, 0, s>>>(a);
 }
 
-// Waves: eight, or four where several row blocks already fill a compute unit's
-// registers (N = 32, R = 2: 11008x4096 14.2 us with four, 17.4 with eight); sixteen
-// where few workgroups leave compute units idle and each has its columns to
-// itself.  One tile ahead: two are behind except with sixteen waves of few tiles
-// (11008x4096 N = 1, R = 1: 9.7 / 10.1 us; 1024x4096, sixteen waves: 5.0 / 4.6).
+// Waves: eight, or four where two workgroups or more come to a compute unit, or
+// the rows' accumulators leave no registers for eight (us, four / eight waves: N = 1,
+// R = 4: 28672x4096 15.0 / 19.0, 28672x8192 28.5 / 31.6, 65536x4096 27.3 / 37.1;
+// one workgroup to a compute unit 20480x5120, R = 5, 15.3 / 12.7; N = 32, R = 2:
+// 11008x4096 14.2 / 17.4).  Sixteen are behind eight (N = 1: 2048x1024 3.3 / 2.7,
+// 1024x28672 15.4 / 15.4, N = 32: 1024x4096 8.3 / 7.1).
+// One tile ahead.  Two where a workgroup has one row block of up to 16 rows, and
+// a wave two tiles or more (one / two ahead, N = 1: 4096x11008 9.8 / 8.6,
+// 1024x28672 18.6 / 15.4, 4096x2048 3.9 / 3.6, of one tile each 4096x1024 3.1 / 3.3;
+// of more row blocks 28672x4096, R = 2, 18.6 / 18.1, 11008x4096 9.9 / 10.5; N = 32:
+// 4096x11008 15.5 / 16.6).
 template <int NB>
 void launch_w4(const W4Args& a, hipStream_t s) {
   const int64_t blocks = a.M / kTileRows;
-  const int r = row_blocks(blocks, NB == 1 ? 1.5 : NB == 2 ? 2.5 : 4.0);
-  if constexpr (NB < 4) {
-    if (blocks <= 128) return launch_w4_as<1, NB, 16, NB == 1 ? 2 : 1>(a, s);
-  }
-  constexpr int kW = NB == 1 ? 8 : 4;
-  switch (r) {
-    case 1: return launch_w4_as<1, NB, 8, 1>(a, s);
-    case 2: return launch_w4_as<2, NB, kW, 1>(a, s);
-    case 3: return launch_w4_as<3, NB, kW, 1>(a, s);
-    case 4: return launch_w4_as<4, NB, kW, 1>(a, s);
-    default: return launch_w4_as<5, NB, kW, 1>(a, s);
+  const int r = row_blocks(blocks, NB);
+  if constexpr (NB == 1) {
+    // Two or five row blocks are one round here, three and four also more.
+    const bool one = blocks <= kComputeUnits * r;
+    switch (r) {
+      case 1: return a.tiles >= 16 ? launch_w4_as<1, NB, 8, 2>(a, s) : launch_w4_as<1, NB, 8, 1>(a, s);
+      case 2: return launch_w4_as<2, NB, 8, 1>(a, s);
+      case 3: return one ? launch_w4_as<3, NB, 8, 1>(a, s) : launch_w4_as<3, NB, 4, 1>(a, s);
+      case 4: return one ? launch_w4_as<4, NB, 8, 1>(a, s) : launch_w4_as<4, NB, 4, 1>(a, s);
+      default: return launch_w4_as<5, NB, 8, 1>(a, s);
+    }
+  } else {
+    switch (r) {
+      case 1: return launch_w4_as<1, NB, 8, 1>(a, s);
+      case 2: return launch_w4_as<2, NB, 4, 1>(a, s);
+      case 3: return launch_w4_as<3, NB, 4, 1>(a, s);
+      case 4: return launch_w4_as<4, NB, 4, 1>(a, s);
+      default: return launch_w4_as<5, NB, 4, 1>(a, s);
+    }
   }
 }
 
