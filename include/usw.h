@@ -915,14 +915,14 @@ usw_status usw_w4_encode(const uint16_t* W, int32_t M, int32_t K, int32_t group,
 usw_status usw_w4_encode_device(const uint16_t* W, int32_t M, int32_t K, int32_t group, void* codes, uint16_t* scales,
                                 void* stream);
 
-/* Workspace of usw_w4_matmul (0 up to 128 or 192 rows, see there) and its leading counter bytes,
- * with usw_spmm_fused_workspace's rules. */
+/* Workspace of usw_w4_matmul (0 up to 128, 192 or 320 rows, see there) and its
+ * leading counter bytes, with usw_spmm_fused_workspace's rules. */
 usw_status usw_w4_matmul_workspace(const usw_w4_fmt* fmt, int32_t N, size_t* bytes, size_t* counter_bytes);
 
 /*
  * Y [N][M] = res + mul * act(W x + bias), X [N][K] fp16, with usw_spmm_fused's
  * epilogue, layouts and rules.  Up to 128 rows (192 of weights of 8192
- * outputs and more) the codes are multiplied as they are read, in passes of up
+ * outputs and more, 320 if K >= 4096 and 2 M K > 192 MiB, too) the codes are multiplied as they are read, in passes of up
  * to 64; more rows take the weight expanded to fp16 in the workspace.  x behind
  * K or N is not read.  Errors: as usw_spmm_fused.
  */

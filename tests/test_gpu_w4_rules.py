@@ -1,6 +1,6 @@
 """GPU tests of the 4-bit product on both sides of its rules: workgroups of one to
-five row blocks, in one round of compute units and in more, one and two tiles ahead.
-Whole inputs make the sums exact."""
+five row blocks, in one round of compute units and in more, one and two tiles ahead,
+and the rows from which a weight is expanded.  Whole inputs make the sums exact."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -10,6 +10,7 @@ if not torch.cuda.is_available():  # pragma: no cover - CPU containers
     pytest.skip("needs a GPU", allow_module_level=True)
 
 import unstructured_sparse_weight_amd as usw  # noqa: E402
+from unstructured_sparse_weight_amd import w4  # noqa: E402
 
 DEV = "cuda:0"
 
@@ -49,4 +50,13 @@ def test_rounds(M):
     """The last row block of a round and the first behind it."""
     enc, W = encoded(M, 320, 128, M)
     for N in (1, 16, 17, 33):
+        check(enc, W, N, N)
+
+
+@pytest.mark.parametrize("M,K,last", [(20480, 5120, 320), (16384, 8192, 320), (24576, 4096, 192), (8192, 4096, 192),
+                                      (8176, 4096, 128)])
+def test_rows_before_expansion(M, K, last):
+    enc, W = encoded(M, K, 64, 3)
+    for N in (last - 64, last - 1, last, last + 1):
+        assert (w4._sizes(M, K, 64, N)[0] > 0) == (N > last)
         check(enc, W, N, N)

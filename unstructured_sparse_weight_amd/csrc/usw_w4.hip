@@ -306,17 +306,25 @@ struct W4Plan {
 };
 
 // Rows of a pass over the codes, and up to which such passes are taken (MI355X,
-// passes / expanded, us: 20480x5120 N = 128 57 / 131, 192 82 / 138, 320 137 / 139;
-// 11008x4096 N = 192 52 / 58, 256 69 / 61; 8192x8192 N = 192 72 / 92, 256 95 / 78;
-// fewer outputs leave compute units without a row block: 4096x11008 N = 128 52 / 51,
-// 160 75 / 57; 4096x4096 N = 128 25.0 / 26.8, 160 35 / 31; 2048x1024 N = 128 14.7 /
-// 16.1, 160 17.7 / 15.8).
+// passes / expanded, us: 8192x8192 N = 192 65 / 74, 193 84 / 74; 11008x4096 N = 192
+// 46 / 58, 193 60 / 58; 16384x4096 N = 192 57 / 69, 193 74 / 69; fewer outputs leave
+// compute units without a row block: 4096x11008 N = 128 52 / 51, 160 75 / 57;
+// 4096x4096 N = 128 25.0 / 26.8, 160 35 / 31; 2048x1024 N = 128 14.7 / 16.1, 160
+// 17.7 / 15.8).  A dense weight of more than 192 MiB, with the codes, does not stay in
+// the 256 MB cache between its expansion and its product: 20480x5120 N = 256 100 /
+// 139, 320 125 / 143, 16384x8192 N = 320 154 / 228, 28672x8192 N = 320 285 / 350,
+// 28672x4096 N = 256 136 / 156, 320 170 / 168; just below, 24576x4096 N = 193 112 /
+// 100, 12288x8192 N = 256 106 / 115.  With few columns a pass is mostly its start:
+// 65536x2048 N = 193 175 / 137, 40960x2560 N = 320 152 / 142.
 constexpr int kPassRows = 64;
-int few_rows(int64_t outputs) { return outputs >= 8192 ? 192 : 128; }
+int few_rows(int64_t outputs, int64_t columns) {
+  if (outputs < 8192) return 128;
+  return columns >= 4096 && outputs * columns * 2 > int64_t(192) << 20 ? 320 : 192;
+}
 
 W4Plan plan_w4(const usw_w4_fmt* f, int32_t N) {
   W4Plan p{};
-  p.wide = N > few_rows(f->M);
+  p.wide = N > few_rows(f->M, f->K);
   if (!p.wide) return p;
   p.g.M = f->M;
   p.g.K = f->K;
