@@ -866,7 +866,10 @@ usw_status usw_spmm_gated_backward_workspace(const usw_fmt* gate, const usw_fmt*
  * above.  The products take dg and du rounded to fp16 (more than 32 rows) or to
  * an fp16 value and the fp16 remainder (up to 32), the biases' sums unrounded.
  * So dg and du share fp16's range with their results: a loss is scaled as for
- * any fp16 gradient.  Infinities of X and of fp16 weights stay infinite where
+ * any fp16 gradient.  One beyond it is infinite, and so is what it adds to dX
+ * and the values, or a NaN where it meets a zero (of an element not kept, too).
+ * A g beyond fp16, kept as an infinity, has its limits act(g) = 0 or infinity,
+ * act'(g) = 0 or 1.  Infinities of X and of fp16 weights stay infinite where
  * |dg| and |du| are 2^-24 and more.  ReLU's slope at 0 is 0.  Rules and errors
  * as usw_spmm_backward.
  */
@@ -922,9 +925,10 @@ usw_status usw_w4_matmul_workspace(const usw_w4_fmt* fmt, int32_t N, size_t* byt
 /*
  * Y [N][M] = res + mul * act(W x + bias), X [N][K] fp16, with usw_spmm_fused's
  * epilogue, layouts and rules.  Up to 128 rows (192 of weights of 8192
- * outputs and more, 320 if K >= 4096 and 2 M K > 192 MiB, too) the codes are multiplied as they are read, in passes of up
- * to 64; more rows take the weight expanded to fp16 in the workspace.  x behind
- * K or N is not read.  Errors: as usw_spmm_fused.
+ * outputs and more, 320 of those if K >= 4096 and 2 M K > 192 MiB) the codes are
+ * multiplied as they are read, in passes of up to 64; more rows take the weight
+ * expanded to fp16 in the workspace.  x behind K or N is not read.  Errors: as
+ * usw_spmm_fused.
  */
 usw_status usw_w4_matmul(const usw_w4_fmt* fmt, const uint16_t* X, void* Y, int32_t y_type, int32_t N,
                          const usw_epilogue* ep, void* ws, size_t ws_bytes, void* stream);

@@ -56,24 +56,28 @@ constexpr int64_t kMaxD = int64_t(1) << 35;          // stay below HIP's 2^32 th
 // ---------------------------------------------------------------------------
 
 // The activation and its slope.  p is the logistic function of v (SiLU) or of
-// 2 z (GELU's tanh form), or the normal distribution's (GELU).
+// 2 z (GELU's tanh form), or the normal distribution's (GELU).  A g beyond fp16 is
+// kept as an infinity, where p is 0 or 1 and its product with v, or 1 - p's, would be
+// a NaN: there the limits are taken, by v's nearest finite fp16 numbers.  A NaN is
+// in p.
 template <int ACT>
 __device__ __forceinline__ void act_and_slope(float v, float* a, float* s) {
+  const float left = fmaxf(v, -65504.0f), near = fminf(left, 65504.0f);
   if constexpr (ACT == USW_ACT_RELU) {
     *a = v < 0.0f ? 0.0f : v;
     *s = v > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == USW_ACT_GELU) {
     const float p = 0.5f * erfcf(v * -0.70710678118654752f);
-    *a = v * p;
-    *s = p + v * (0.39894228040143268f * __expf(-0.5f * v * v));
+    *a = left * p;
+    *s = p + near * (0.39894228040143268f * __expf(-0.5f * v * v));
   } else if constexpr (ACT == USW_ACT_GELU_TANH) {
     const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
-    *a = v * p;
-    *s = p + v * (1.5957691216057308f * (1.0f + 0.134145f * v * v)) * (p * (1.0f - p));
+    *a = left * p;
+    *s = p + near * (1.5957691216057308f * (1.0f + 0.134145f * near * near)) * (p * (1.0f - p));
   } else if constexpr (ACT == USW_ACT_SILU) {
     const float p = __builtin_amdgcn_rcpf(1.0f + __expf(-v));
-    *a = v * p;
-    *s = p + v * (p * (1.0f - p));
+    *a = left * p;
+    *s = p + near * (p * (1.0f - p));
   } else {
     *a = v;
     *s = 1.0f;
