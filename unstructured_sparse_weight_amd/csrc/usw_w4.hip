@@ -22,7 +22,7 @@
 //   * The waves of a workgroup share a strip of 16 R rows and split its
 //     columns; their sums meet in LDS in a fixed order, so no such call needs a
 //     workspace and results do not depend on timing.
-// 20480x5120 N = 16: 57 MB in 16.3 us, 3.5 TB/s; 11008x4096 N = 1 8.4.
+// 20480x5120 N = 16: 57 MB in 15.2 us, 3.7 TB/s; 11008x4096 N = 1 8.2.
 // Many rows: the weight is expanded to dense fp16 fragments and multiplied as
 // the sparse weights are (usw_wide.hip).
 #include <hip/hip_runtime.h>

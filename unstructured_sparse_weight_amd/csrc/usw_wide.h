@@ -45,9 +45,14 @@ struct WidePlan {
   size_t cb, slots_at, dense_at, need;   // workspace: counters (0: none), partial sums, dense fragments
 };
 
-// lone: large tiles also where there is no whole round of them (all their
-// columns are shared then): the gradient of 11008x4096 pairs, N = 2048, whose
-// product has 128 of them over 344 columns, 853 us with large, 925 with medium.
+// lone: large tiles also where there is no whole round of them and the estimate has
+// them ahead (all their columns are shared then).  Calls with / without, us: gated
+// 5120x5120 N = 1500 182 / 200, 2048x8192 N = 2000 144 / 155; gradients of pairs of
+// 11008x4096 N = 1024 483 / 561, 8192x2048 N = 2000 323 / 363, INT4 20480x5120 N = 400
+// 422 / 617; 4-bit 4096x11008 N = 2047 190 / 210, 5120x20480 N = 512 211 / 283; where
+// the estimate has medium tiles ahead both are one, 4-bit 4096x4096 N = 2048 77.6 /
+// 76.7.  None was slower; the fused and expert products go without, because sums of
+// shared columns are added in another order and their results are kept bit for bit.
 WidePlan wide_plan(const Geometry& g, int32_t E, int32_t S, bool lone = false);
 
 // Whether the plan's product is a launch: less than HIP's 2^32 threads, 256 of
