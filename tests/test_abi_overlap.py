@@ -67,6 +67,13 @@ def test_overlapping_outputs_are_refused(call, read, out):
             assert call(p) == UNSUPPORTED, (o, r, "end")
 
 
+def test_neighbours_are_taken():
+    """The buffers of Places, each where the one before ends: the call goes on to launch, which fails without a GPU."""
+    for call in (single, pair):
+        for i4 in (False, True):
+            assert call(Places(i4), i4) not in (UNSUPPORTED, 0)
+
+
 def test_int4_scales_and_x():
     """INT4 has no values' gradient, so x is not read; its scales are."""
     for call in (single, pair):

@@ -51,7 +51,7 @@ struct WidePlan {
 // 11008x4096 N = 1024 483 / 561, 8192x2048 N = 2000 323 / 363, INT4 20480x5120 N = 400
 // 422 / 617; 4-bit 4096x11008 N = 2047 190 / 210, 5120x20480 N = 512 211 / 283; where
 // the estimate has medium tiles ahead both are one, 4-bit 4096x4096 N = 2048 77.6 /
-// 76.7.  None was slower; the fused and expert products go without, because sums of
+// 76.7.  None was slower by more than 1%; the fused and expert products go without, because sums of
 // shared columns are added in another order and their results are kept bit for bit.
 WidePlan wide_plan(const Geometry& g, int32_t E, int32_t S, bool lone = false);
 
